@@ -1,0 +1,519 @@
+"""Cases of the operators around the feed-forward layer: the residual sum with
+dropout and root-mean-square norm (forward, backward, 8-bit output), dropout
+with a residual, 4-bit matrix-vector products and the few-token feed-forward
+layer on 4-bit weights.
+
+`run` computes a case in elementary torch operations, or, with `own` set,
+through the package's entry points.  The formats both sides read and write:
+
+  MXFP8   e4m3 codes [T][d] and one e8m0 scale per 32 columns; the scale is the
+          smallest power of two that holds the group's largest value within
+          +-448 (an all-zero group has scale byte 0)
+  MXFP4   e2m1 codes, two per byte along a row (even column in the low four
+          bits), and one e8m0 scale per 32 columns
+  dropout Philox4x32 of ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel
+          random numbers: as easy as 1, 2, 3", 2011); key = seed, counter =
+          (block, offset), one block per eight columns of a row: column c of
+          row t is the 16-bit half c % 8 of block t * ceil(d / 8) + c / 8, and
+          is dropped where it lies below round(65536 p)
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+EPS = 1e-5
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+FP4 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+PHILOX_M = (0xD2511F53, 0xCD9E8D57)
+PHILOX_W = (0x9E3779B9, 0xBB67AE85)
+
+
+# ---------------------------------------------------------------- the cases
+
+def _norm(name, T, d, x, res, y, p):
+    return {"name": name, "op": "norm", "T": T, "d": d, "x": x, "res": res, "y": y, "p": p}
+
+
+def _norm_bwd(name, T, d, dy, res, dx, p):
+    return {"name": name, "op": "norm_bwd", "T": T, "d": d, "y": dy, "res": res, "x": dx, "p": p}
+
+
+def _drop(name, T, d, x, res, y, p):
+    return {"name": name, "op": "dropout", "T": T, "d": d, "x": x, "res": res, "y": y, "p": p}
+
+
+def _matvec(name, T, N, K, x, y):
+    return {"name": name, "op": "matvec", "T": T, "N": N, "K": K, "x": x, "y": y}
+
+
+def _ffn(name, T, d, F, x, y, density):
+    return {"name": name, "op": "ffn", "T": T, "d": d, "F": F, "x": x, "y": y, "density": density}
+
+
+def listed():
+    return [
+        # one decoded token ahead of the 2b-sized layer: pure latency
+        _norm("norm, one token, to 8 bits", 1, 2304, "f32", "bf16", "mx8", 0.0),
+        # a ragged prompt chunk of the 1.5b-sized layer, written as 8 bits
+        _norm("norm, prompt, to 8 bits", 2047, 2048, "bf16", "bf16", "mx8", 0.0),
+        # a training batch at the 2b sizes: the layer's fp32 output is dropped,
+        # added to the bf16 residual stream and normed for the next layer
+        _norm("norm, training, dropout", 32768, 2304, "f32", "bf16", "bf16", 0.1),
+        # fp32 throughout, odd width
+        _norm("norm, odd width, f32", 1003, 1001, "f32", "f32", "f32", 0.0),
+        # the gradient of the training batch: dy is the layer's fp32 dX
+        _norm_bwd("norm backward, training", 32768, 2304, "f32", "bf16", "bf16", 0.1),
+        # the gradient of an odd, small fp32 batch
+        _norm_bwd("norm backward, odd, f32", 777, 1001, "f32", "f32", "f32", 0.25),
+        # the last layer's output added to the residual stream, 1.5b sizes
+        _drop("dropout with residual", 16384, 2048, "bf16", "bf16", "bf16", 0.1),
+        # the gradient's way through dropout, small and odd
+        _drop("dropout backward, odd", 333, 1001, "f32", "none", "f32", 0.25),
+        # one token through one projection of the 2b sizes
+        _matvec("4-bit matvec, one token", 1, 9216, 2304, "bf16", "f32"),
+        # a batch of tokens into a wide output layer of odd size
+        _matvec("4-bit product, 16 tokens, wide", 16, 40001, 2048, "mx8", "f32"),
+        # one decoded token through the 2b-sized layer
+        _ffn("4-bit layer, one token", 1, 2304, 9216, "mx8", "f32", 0.0093),
+        # a decode batch through the 1.5b-sized layer
+        _ffn("4-bit layer, 64 tokens", 64, 2048, 5632, "bf16", "bf16", 0.015),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """An integer of lo..hi, even over the logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(("norm", "norm", "norm_bwd", "dropout", "matvec", "ffn"))
+    if op in ("norm", "norm_bwd", "dropout"):
+        # widths from 64 to 8192, a third of them of any remainder; rows up to
+        # the largest listed batch's number of values
+        d = _spread(rng, 64, 8192)
+        if rng.random() < 2 / 3:
+            d = max(64, d // 64 * 64)
+        T = _spread(rng, 1, max(1, min(32768, 32768 * 2304 // d)))
+        x, res = rng.choice(("f32", "bf16")), rng.choice(("f32", "bf16"))
+        p = rng.choice((0.0, 0.1, 0.25, 0.5))
+        if op == "norm":
+            y = rng.choice(("f32", "bf16", "mx8"))
+            c = _norm("", T, d, x, res, y, 0.0 if y == "mx8" else p)
+        elif op == "norm_bwd":
+            c = _norm_bwd("", T, d, rng.choice(("f32", "bf16")), res, x, p)
+        else:
+            c = _drop("", T, d, x, rng.choice(("none", "f32", "bf16")), rng.choice(("f32", "bf16")), max(p, 0.1))
+    elif op == "matvec":
+        K = 32 * _spread(rng, 8, 512)
+        N = _spread(rng, 256, min(65536, 40001 * 2048 // K))
+        c = _matvec("", _spread(rng, 1, 64), N, K, rng.choice(("bf16", "mx8")), rng.choice(("f32", "bf16")))
+    else:
+        d = 64 * _spread(rng, 4, 64)
+        F = 64 * _spread(rng, 8, min(256, 40001 * 2048 // (3 * 64 * d)))
+        c = _ffn("", _spread(rng, 1, 64), d, F, rng.choice(("bf16", "mx8")), rng.choice(("f32", "bf16")),
+                 rng.choice((0.0093, 0.015, 0.03)))
+    del c["name"]
+    return c
+
+
+# ---------------------------------------------------------------- inputs
+
+def _normal(g, *size):
+    return torch.randn(*size, generator=g, device="cuda")
+
+
+def _rng_state(g):
+    """Seed and offset of one dropout call: two 64-bit numbers on the device."""
+    return torch.randint(0, 1 << 62, (2,), generator=g, device="cuda", dtype=torch.int64)
+
+
+def _stream(g, T, d, dt):
+    """A residual stream: a few channels are much larger than the rest."""
+    s = _normal(g, T, d)
+    s *= torch.exp(0.7 * _normal(g, d))
+    return s.to(dt)
+
+
+def _pow2(e):
+    """2**e in fp32 for whole e of -149..127."""
+    return torch.ldexp(torch.ones((), device=e.device), e)
+
+
+def _to_mx(v, top, small):
+    """(v / scale, scale's byte) by groups of 32 columns: the scale is the
+    smallest power of two with max|v| <= top * scale, top = frac * 2**exp."""
+    frac, exp = math.frexp(top)
+    T, K = v.shape
+    pad = -K % 32
+    v = torch.nn.functional.pad(v, (0, pad)).view(T, -1, 32)
+    m = v.abs().amax(dim=-1)
+    f, e = torch.frexp(m)
+    e = torch.where(f <= frac, e - exp, e - exp + 1)
+    e = torch.where(m == 0, -127, e.clamp(-127, 127))
+    q = torch.ldexp(v, -e.unsqueeze(-1)).view(T, -1)[:, :K]
+    return (q if small is None else small(q)), (e + 127).to(torch.uint8)
+
+
+def _fp4_codes(q):
+    """Nearest e2m1 code of each value, ties to the even code."""
+    a = q.abs()
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
+    return code | ((q < 0).to(torch.uint8) << 3)
+
+
+def _weights(g, N, K, std):
+    """MXFP4 codes [N][K/2] and scales [N][K/32] of normal weights."""
+    codes = torch.empty(N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(N, K // 32, dtype=torch.uint8, device="cuda")
+    for n in range(0, N, 8192):
+        q, s = _to_mx(std * _normal(g, min(8192, N - n), K), 6.0, _fp4_codes)
+        codes[n:n + 8192] = q[:, 0::2] | (q[:, 1::2] << 4)
+        scales[n:n + 8192] = s
+    return codes, scales
+
+
+def _tokens(g, T, K, kind):
+    """Normed activations as bf16 (x, None) or as MXFP8 (codes, scales)."""
+    x = _normal(g, T, K)
+    if kind == "bf16":
+        return x.bfloat16(), None
+    q, s = _to_mx(x, 448.0, None)
+    return q.to(torch.float8_e4m3fn), s
+
+
+def _gate_bias(g, F, density):
+    """Biases under which neuron n fires on a share p_n of normal tokens with
+    unit-norm weight rows: p_n falls with a power of the neuron's rank, and a
+    tenth of the neurons never fires."""
+    rank = torch.randperm(F, generator=g, device="cuda").double() + 1
+    w = torch.where(rank > 0.9 * F, 0.0, rank ** -1.1)
+    lo, hi = 0.0, float(F)
+    for _ in range(60):
+        c = (lo + hi) / 2
+        lo, hi = (c, hi) if float((c * w).clamp(max=0.99).mean()) < density else (lo, c)
+    p = (hi * w).clamp(max=0.99)
+    return torch.where(p > 0, math.sqrt(2) * torch.erfinv(2 * p - 1), -1e4).bfloat16()
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    s = {"case": case}
+    if case["op"] in ("norm", "norm_bwd", "dropout"):
+        T, d = case["T"], case["d"]
+        s["rng"] = _rng_state(g)
+        if case["op"] == "norm":
+            s["x"] = _normal(g, T, d).to(DT[case["x"]])
+            s["res"] = _stream(g, T, d, DT[case["res"]])
+            s["w"] = (1 + 0.1 * _normal(g, d)).to(DT[case["res"]])
+        elif case["op"] == "norm_bwd":
+            s["dy"] = _normal(g, T, d).to(DT[case["y"]])
+            s["dsum"] = _normal(g, T, d).to(DT[case["res"]])
+            s["sum"] = _stream(g, T, d, DT[case["res"]])
+            s["w"] = (1 + 0.1 * _normal(g, d)).to(DT[case["res"]])
+            s["rstd"] = torch.rsqrt(s["sum"].double().square().mean(dim=1) + EPS).float()
+        else:
+            s["x"] = _normal(g, T, d).to(DT[case["x"]])
+            s["res"] = None if case["res"] == "none" else _stream(g, T, d, DT[case["res"]])
+    elif case["op"] == "matvec":
+        s["x"], s["xs"] = _tokens(g, case["T"], case["K"], case["x"])
+        s["W"] = _weights(g, case["N"], case["K"], case["K"] ** -0.5)
+        s["bias"] = (0.1 * _normal(g, case["N"])).bfloat16()
+    else:
+        d, F = case["d"], case["F"]
+        s["x"], s["xs"] = _tokens(g, case["T"], d, case["x"])
+        s["Wg"] = _weights(g, F, d, d ** -0.5)
+        s["Wu"] = _weights(g, F, d, d ** -0.5)
+        s["Wd"] = _weights(g, F, d, F ** -0.5)
+        s["bg"] = _gate_bias(g, F, case["density"])
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _philox_words(rng, blocks):
+    """The four 32-bit words (int64 tensors) of the counters (block, offset)
+    under the key `seed`.  Products wrap modulo 2**64, which leaves the upper
+    word of a 32 x 32-bit product in bits 32..63."""
+    low = 0xFFFFFFFF
+    k0, k1 = rng[0] & low, (rng[0] >> 32) & low
+    c0, c1 = blocks & low, (blocks >> 32) & low
+    c2, c3 = (rng[1] & low).expand_as(c0), ((rng[1] >> 32) & low).expand_as(c0)
+    for _ in range(10):      # the generator's rounds
+        a, b = c0 * PHILOX_M[0], c2 * PHILOX_M[1]
+        c0, c1, c2, c3 = ((b >> 32) & low) ^ c1 ^ k0, b & low, ((a >> 32) & low) ^ c3 ^ k1, a & low
+        k0, k1 = (k0 + PHILOX_W[0]) & low, (k1 + PHILOX_W[1]) & low
+    return c0, c1, c2, c3
+
+
+def _keep(rng, T, d, p):
+    """Which values of a [T][d] matrix dropout keeps."""
+    nb = -(-d // 8)
+    words = torch.stack(_philox_words(rng, torch.arange(T * nb, device="cuda")), dim=-1)
+    halves = torch.stack((words & 0xFFFF, words >> 16), dim=-1)
+    return halves.view(T, nb * 8)[:, :d] >= round(65536 * p)
+
+
+def _dropped(x, rng, p):
+    if p == 0:
+        return x
+    thr = round(65536 * p)
+    return torch.where(_keep(rng, *x.shape, p), x * (65536 / (65536 - thr)), 0.0)
+
+
+def _plain_norm(s, case):
+    v = _dropped(s["x"].float(), s["rng"], case["p"]) + s["res"].float()
+    total = v.to(DT[case["res"]])
+    v = total.float()
+    rstd = torch.rsqrt(v.square().mean(dim=1) + EPS)
+    y = v * rstd[:, None] * s["w"].float()
+    if case["y"] != "mx8":
+        return {"sum": total, "y": y.to(DT[case["y"]]), "rstd": rstd}
+    q, scale = _to_mx(y, 448.0, None)
+    return {"sum": total, "y": q.to(torch.float8_e4m3fn), "scale": scale.view(torch.float8_e8m0fnu)}
+
+
+def _plain_norm_bwd(s, case):
+    dy, v, w = s["dy"].float(), s["sum"].float(), s["w"].float()
+    r = s["rstd"][:, None]
+    xhat, wdy = v * r, dy * w
+    c = (wdy * xhat).mean(dim=1, keepdim=True)
+    dres = r * (wdy - xhat * c) + s["dsum"].float()
+    dx = _dropped(dres, s["rng"], case["p"])
+    return {"dres": dres.to(DT[case["res"]]), "dx": dx.to(DT[case["x"]]), "dw": (dy * xhat).sum(dim=0)}
+
+
+def _plain_dropout(s, case):
+    v = _dropped(s["x"].float(), s["rng"], case["p"])
+    return (v if s["res"] is None else v + s["res"].float()).to(DT[case["y"]])
+
+
+def _plain_w4(w):
+    """fp32 values of MXFP4 weights."""
+    codes, scales = w
+    N = codes.shape[0]
+    q = torch.stack((codes & 15, codes >> 4), dim=-1).view(N, -1, 32)
+    v = torch.tensor(FP4 + tuple(-f for f in FP4), device=codes.device)[q.int()]
+    return (v * _pow2(scales.int() - 127)[:, :, None]).view(N, -1)
+
+
+def _plain_tokens(s):
+    if s["xs"] is None:
+        return s["x"].float()
+    v = s["x"].float()
+    e = (s["xs"].int() - 127).repeat_interleave(32, dim=1)[:, :v.shape[1]]
+    return v * _pow2(e)
+
+
+def _plain_matvec(s, case):
+    return (_plain_tokens(s) @ _plain_w4(s["W"]).t() + s["bias"].float()).to(DT[case["y"]])
+
+
+def _plain_ffn(s, case):
+    x = _plain_tokens(s)
+    h = (x @ _plain_w4(s["Wg"]).t() + s["bg"].float()).clamp(min=0)
+    u = x @ _plain_w4(s["Wu"]).t()
+    return ((h * u) @ _plain_w4(s["Wd"])).to(DT[case["y"]])
+
+
+PLAIN = {"norm": _plain_norm, "norm_bwd": _plain_norm_bwd, "dropout": _plain_dropout, "matvec": _plain_matvec,
+         "ffn": _plain_ffn}
+
+
+# ---------------------------------------------------------------- the package's calls
+
+def _rows(*size, dt):
+    return torch.empty(*size, dtype=dt, device="cuda")
+
+
+def _plan(s, case):
+    """The output buffers, shape and workspace that a user's program keeps with
+    its inputs from call to call."""
+    import activation_sparse_feedforward_gate_amd as tw
+    dt = {"f32": tw.TWELL_F32, "bf16": tw.TWELL_BF16, "mx8": tw.TWELL_MXFP8, "none": tw.TWELL_F32}
+    op, b = case["op"], {"tw": tw}
+    if op in ("norm", "norm_bwd", "dropout"):
+        T, d = case["T"], case["d"]
+        b["shape"] = tw.norm_shape(T, d, x_dt=dt[case["x"]], res_dt=dt[case["res"]], y_dt=dt[case["y"]],
+                                   w_dt=dt[case["res"]], eps=EPS, p=case["p"])
+        if op == "norm":
+            b["sum"] = _rows(T, d, dt=DT[case["res"]])
+            if case["y"] == "mx8":
+                b["y"], b["scale"] = _rows(T, d, dt=torch.float8_e4m3fn), _rows(T, -(-d // 32), dt=torch.uint8)
+                b["out"] = {"sum": b["sum"], "y": b["y"], "scale": b["scale"].view(torch.float8_e8m0fnu)}
+                b["rstd"] = None
+            else:
+                b["y"], b["scale"], b["rstd"] = _rows(T, d, dt=DT[case["y"]]), None, _rows(T, dt=torch.float32)
+                b["out"] = {"sum": b["sum"], "y": b["y"], "rstd": b["rstd"]}
+        elif op == "norm_bwd":
+            b["dres"], b["dx"] = _rows(T, d, dt=DT[case["res"]]), _rows(T, d, dt=DT[case["x"]])
+            b["dw"] = _rows(d, dt=torch.float32)
+            b["ws"] = _rows(max(16, tw.twell_add_rmsnorm_bwd_workspace(b["shape"])), dt=torch.uint8)
+            b["out"] = {"dres": b["dres"], "dx": b["dx"], "dw": b["dw"]}
+        else:
+            b["out"] = _rows(T, d, dt=DT[case["y"]])
+    elif op == "matvec":
+        b["W"] = tw.TwellW4(*s["W"])
+        b["out"] = _rows(case["T"], case["N"], dt=DT[case["y"]])
+    else:
+        T, d, F = case["T"], case["d"], case["F"]
+        b["shape"] = tw.ffn_shape(T, d, F, dt[case["x"]], dt[case["y"]])
+        b["Wg"], b["Wu"], b["Wd"] = (tw.TwellW4(*s[k]) for k in ("Wg", "Wu", "Wd"))
+        b["ws"] = _rows(max(16, tw.twell_ffn_fwd_w4_workspace(b["shape"])), dt=torch.uint8)
+        b["out"] = _rows(T, d, dt=DT[case["y"]])
+    return b
+
+
+def _own_run(s, case):
+    b = s.get("plan") or s.setdefault("plan", _plan(s, case))
+    tw, op = b["tw"], case["op"]
+    if op == "norm":
+        tw.twell_add_rmsnorm_fwd(b["shape"], s["x"], s["res"], s["w"], s["rng"], b["sum"], b["y"], b["scale"],
+                                 b["rstd"])
+    elif op == "norm_bwd":
+        tw.twell_add_rmsnorm_bwd(b["shape"], s["dy"], s["dsum"], s["sum"], s["w"], s["rstd"], s["rng"], b["dres"],
+                                 b["dx"], b["dw"], b["ws"])
+    elif op == "dropout":
+        tw.twell_dropout_add(b["shape"], s["x"], s["res"], s["rng"], b["out"])
+    elif op == "matvec":
+        tw.twell_w4_matvec(s["x"], s["xs"], b["W"], s["bias"], b["out"])
+    else:
+        tw.twell_ffn_fwd_w4(b["shape"], s["x"], s["xs"], b["Wg"], s["bg"], b["Wu"], b["Wd"], b["out"], b["ws"])
+    return b["out"]
+
+
+def run(state):
+    case = state["case"]
+    return _own_run(state, case) if own else PLAIN[case["op"]](state, case)
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+SIZE = {"f32": 4, "bf16": 2, "none": 0}
+
+
+def work(case):
+    op = case["op"]
+    if op in ("norm", "norm_bwd", "dropout"):
+        T, d = case["T"], case["d"]
+        n = T * d
+        y = n + T * -(-d // 32) if case["y"] == "mx8" else n * SIZE[case["y"]]
+        if op == "norm":
+            return {"bytes": n * (SIZE[case["x"]] + 2 * SIZE[case["res"]]) + y + d * SIZE[case["res"]]
+                    + (0 if case["y"] == "mx8" else 4 * T), "flops": 6 * n}
+        if op == "norm_bwd":
+            return {"bytes": y + n * (3 * SIZE[case["res"]] + SIZE[case["x"]]) + 4 * T
+                    + d * (4 + SIZE[case["res"]]), "flops": 12 * n}
+        return {"bytes": n * (SIZE[case["x"]] + SIZE[case["res"]]) + y, "flops": 2 * n}
+    T = case["T"]
+    if op == "matvec":
+        N, K = case["N"], case["K"]
+        x = 2 * T * K if case["x"] == "bf16" else T * K + T * K // 32
+        return {"bytes": N * K // 2 + N * K // 32 + x + 2 * N + T * N * SIZE[case["y"]], "flops": 2 * T * N * K}
+    d, F = case["d"], case["F"]
+    x = 2 * T * d if case["x"] == "bf16" else T * d + T * d // 32
+    # the gate reads every neuron; the other two weights' rows are needed where
+    # a token fires the neuron
+    fired = _fired(F, case["density"], T)
+    row = d // 2 + d // 32
+    return {"bytes": F * row + 2 * fired * row + x + 2 * F + T * d * SIZE[case["y"]],
+            "flops": 2 * T * F * d + 4 * T * F * case["density"] * d}
+
+
+def _fired(F, density, T):
+    """Expected number of neurons that at least one of T tokens fires."""
+    rank = np.arange(1, F + 1)
+    w = np.where(rank > 0.9 * F, 0.0, rank ** -1.1)
+    lo, hi = 0.0, float(F)
+    for _ in range(60):
+        c = (lo + hi) / 2
+        lo, hi = (c, hi) if np.minimum(c * w, 0.99).mean() < density else (lo, c)
+    return float((1 - (1 - np.minimum(hi * w, 0.99)) ** T).sum())
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+def _exact_keep(rng, T, d, p):
+    """The kept values, from the generator's definition on 64-bit unsigned
+    words of numpy, in slices of rows."""
+    seed, off = (int(v) & (2 ** 64 - 1) for v in rng.tolist())
+    nb, u = -(-d // 8), np.uint64
+    keep = np.empty((T, d), dtype=bool)
+    low, sh = u(0xFFFFFFFF), u(32)
+    step = max(1, (1 << 20) // nb)
+    for t in range(0, T, step):
+        n = min(step, T - t)
+        i = np.arange(t * nb, (t + n) * nb, dtype=np.uint64)
+        c = [i & low, i >> sh, np.full_like(i, off & 0xFFFFFFFF), np.full_like(i, off >> 32)]
+        k = [seed & 0xFFFFFFFF, seed >> 32]
+        for _ in range(10):
+            p0, p1 = c[0] * u(0xD2511F53), c[2] * u(0xCD9E8D57)
+            c = [(p1 >> sh) ^ c[1] ^ u(k[0]), p1 & low, (p0 >> sh) ^ c[3] ^ u(k[1]), p0 & low]
+            k = [(k[0] + 0x9E3779B9) % 2 ** 32, (k[1] + 0xBB67AE85) % 2 ** 32]
+        w = np.stack(c, axis=1).astype(np.uint32)
+        h = np.stack((w & np.uint32(0xFFFF), w >> np.uint32(16)), axis=2).reshape(n, nb * 8)
+        keep[t:t + n] = h[:, :d] >= int(round(65536 * p))
+    return torch.from_numpy(keep).cuda()
+
+
+def _exact_drop(v, s, case):
+    p = case["p"]
+    if p == 0:
+        return v
+    share = 1 - int(round(65536 * p)) / 65536
+    return v.div(share).masked_fill(~_exact_keep(s["rng"], *v.shape, p), 0.0)
+
+
+def _exact_weights(w):
+    """e2m1 by its fields: sign, two exponent bits, one mantissa bit."""
+    codes, scales = w
+    N, half = codes.shape
+    q = torch.empty(N, 2 * half, dtype=torch.int32, device=codes.device)
+    q[:, 0::2], q[:, 1::2] = codes.int() % 16, codes.int() // 16
+    e, m = (q // 2) % 4, (q % 2).double()
+    v = torch.where(e == 0, m / 2, (1 + m / 2) * torch.pow(2.0, (e - 1).double()))
+    v = torch.where(q >= 8, -v, v)
+    return v * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, dim=1)
+
+
+def _exact_tokens(s):
+    if s["xs"] is None:
+        return s["x"].double()
+    return s["x"].double() * torch.pow(2.0, s["xs"].double() - 127).repeat_interleave(32, dim=1)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "norm":
+        v = _exact_drop(s["x"].double(), s, case) + s["res"].double()
+        if case["res"] == "bf16":        # the stream is stored in 16 bits and the norm is that of what is stored
+            v = v.bfloat16().double()
+        y = v / (v.square().mean(dim=1, keepdim=True) + EPS).sqrt() * s["w"].double()
+        if case["y"] != "mx8":
+            return {"sum": v, "y": y, "rstd": (v.square().mean(dim=1) + EPS).rsqrt()}
+        T, d = y.shape
+        groups = torch.nn.functional.pad(y, (0, -d % 32)).view(T, -1, 32)
+        top = groups.abs().amax(dim=2)
+        e = torch.ceil(torch.log2(top / 448)).clamp(min=-127)
+        q = (groups / torch.pow(2.0, e)[:, :, None]).view(T, -1)[:, :d]
+        step = torch.pow(2.0, torch.floor(torch.log2(q.abs())).clamp(min=-6) - 3)      # e4m3: three mantissa bits
+        return {"sum": v, "y": torch.round(q / step) * step, "scale": torch.pow(2.0, e)}
+    if op == "norm_bwd":
+        dy, v, w, r = s["dy"].double(), s["sum"].double(), s["w"].double(), s["rstd"].double()[:, None]
+        g = dy * w
+        dot = (g * v).sum(dim=1, keepdim=True)
+        dres = g * r - v * dot * r ** 3 / case["d"] + s["dsum"].double()
+        return {"dres": dres, "dx": _exact_drop(dres, s, case), "dw": (dy * v * r).sum(dim=0)}
+    if op == "dropout":
+        v = _exact_drop(s["x"].double(), s, case)
+        return v if s["res"] is None else s["res"].double() + v
+    x = _exact_tokens(s)
+    if op == "matvec":
+        return torch.nn.functional.linear(x, _exact_weights(s["W"]), s["bias"].double())
+    gate = torch.nn.functional.linear(x, _exact_weights(s["Wg"]), s["bg"].double())
+    a = torch.where(gate > 0, gate * torch.nn.functional.linear(x, _exact_weights(s["Wu"])), 0.0)
+    return a.mm(_exact_weights(s["Wd"]))
