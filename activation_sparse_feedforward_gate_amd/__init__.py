@@ -19,4 +19,6 @@ from ._lib import (  # noqa: F401
     twell_ffn_fwd_bounded_workspace, twell_ffn_fwd_bounded,
     twell_ffn_fwd_compact_workspace, twell_ffn_fwd_compact,
     twell_relu_ffn_fwd_bounded_workspace, twell_relu_ffn_fwd_bounded,
+    TWELL_MXFP8, c_twell_norm_shape, norm_shape, twell_add_rmsnorm_fwd, twell_add_rmsnorm_bwd_workspace,
+    twell_add_rmsnorm_bwd, twell_dropout_add,
 )

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(PKG, "lib", "libtwell.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "twell.h")
 
 TWELL_OK, TWELL_EINVAL, TWELL_EUNSUPPORTED, TWELL_EWORKSPACE, TWELL_EHIP = range(5)
-TWELL_F32, TWELL_BF16 = 0, 1
+TWELL_F32, TWELL_BF16, TWELL_MXFP8 = 0, 1, 2
 R_TILE, C_TILE = 16, 64
 
 
@@ -40,6 +40,11 @@ class c_twell_cmat(ctypes.Structure):
 class c_twell_ffn_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("in_dt", ctypes.c_int), ("out_dt", ctypes.c_int)]
+
+
+class c_twell_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("x_dt", ctypes.c_int), ("res_dt", ctypes.c_int),
+                ("y_dt", ctypes.c_int), ("w_dt", ctypes.c_int), ("eps", ctypes.c_float), ("p", ctypes.c_float)]
 
 
 _lib = None
@@ -106,6 +111,13 @@ def lib() -> ctypes.CDLL:
         L.twell_ffn_fwd_bounded_workspace.argtypes = [P(c_twell_ffn_shape), i32, i32]
         L.twell_ffn_fwd_bounded_workspace.restype = sz
         L.twell_ffn_fwd_bounded.argtypes = [P(c_twell_ffn_shape), vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp]
+        NS = P(c_twell_norm_shape)
+        L.twell_add_rmsnorm_fwd.argtypes = [NS, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp]
+        L.twell_add_rmsnorm_bwd_workspace.argtypes = [NS]
+        L.twell_add_rmsnorm_bwd_workspace.restype = sz
+        L.twell_add_rmsnorm_bwd.argtypes = [NS, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, sz,
+                                            vp]
+        L.twell_dropout_add.argtypes = [NS, vp, i64, vp, i64, vp, vp, i64, vp]
         L.twell_status_string.argtypes = [ctypes.c_int]
         L.twell_status_string.restype = ctypes.c_char_p
         L.twell_last_error.argtypes = []
@@ -116,7 +128,8 @@ def lib() -> ctypes.CDLL:
                      "twell_ffn_dense_fwd", "twell_ffn_dense_bwd",
                      "twell_gate_pack",
                      "twell_sparse_up", "twell_sparse_down", "twell_ffn_fwd_noalloc", "twell_ffn_fwd_bounded",
-                     "twell_ffn_fwd_compact", "twell_relu_ffn_fwd_bounded"):
+                     "twell_ffn_fwd_compact", "twell_relu_ffn_fwd_bounded", "twell_add_rmsnorm_fwd",
+                     "twell_add_rmsnorm_bwd", "twell_dropout_add"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -452,6 +465,75 @@ def twell_ffn_dense_bwd(shape, x, WgT, bg, WuT, Wd, dY, y, dX, dWgT, dWuT, dWd, 
                                      _ptr(dY), _ptr(y), _ptr(dX), _ptr(dWgT), _ptr(dWuT), _ptr(dWd), _ptr(dbg),
                                      _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the layer
+
+def norm_shape(T: int, d: int, x_dt: int, res_dt: int, y_dt: int, w_dt: int, eps: float = 1e-6,
+               p: float = 0.0) -> c_twell_norm_shape:
+    """Shape, dtypes and constants of the residual-sum, norm and dropout calls
+    (twell_norm_shape in include/twell.h)."""
+    return c_twell_norm_shape(T, d, x_dt, res_dt, y_dt, w_dt, eps, p)
+
+
+def _mat(t, T: int, d: int, size: int, name: str):
+    """(pointer, row stride) of a [T][d] matrix with contiguous rows of
+    `size`-byte elements."""
+    if t is None:
+        return None, 0
+    if t.shape != (T, d) or t.element_size() != size or (d > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected [{T}][{d}] of {size}-byte elements with contiguous rows, got "
+                         f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _vec(t, n: int, size: int, name: str):
+    if t is None:
+        return None
+    if t.numel() != n or t.element_size() != size or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous {size}-byte elements, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+_SIZE = {TWELL_F32: 4, TWELL_BF16: 2, TWELL_MXFP8: 1}
+
+
+def _size(dt: int) -> int:
+    return _SIZE.get(dt, 1)
+
+
+def twell_add_rmsnorm_fwd(shape: c_twell_norm_shape, x, residual, w, rng, sum, y, y_scale=None, rstd=None,
+                          stream=None) -> None:
+    """sum = residual + dropout(x); y = its root-mean-square norm times w."""
+    T, d, res = shape.T, shape.d, _size(shape.res_dt)
+    _check(lib().twell_add_rmsnorm_fwd(
+        shape, *_mat(x, T, d, _size(shape.x_dt), "x"), *_mat(residual, T, d, res, "residual"),
+        _vec(w, d, _size(shape.w_dt), "w"), _vec(rng, 2, 8, "rng"), *_mat(sum, T, d, res, "sum"),
+        *_mat(y, T, d, _size(shape.y_dt), "y"), _vec(y_scale, T * -(-d // 32), 1, "y_scale"),
+        _vec(rstd, T, 4, "rstd"), _stream(stream)))
+
+
+def twell_add_rmsnorm_bwd_workspace(shape: c_twell_norm_shape) -> int:
+    return int(lib().twell_add_rmsnorm_bwd_workspace(shape))
+
+
+def twell_add_rmsnorm_bwd(shape: c_twell_norm_shape, dy, dsum, sum, w, rstd, rng, dres, dx, dw, ws,
+                          stream=None) -> None:
+    """The gradients of twell_add_rmsnorm_fwd from its stored sum and rstd."""
+    T, d, res = shape.T, shape.d, _size(shape.res_dt)
+    _check(lib().twell_add_rmsnorm_bwd(
+        shape, *_mat(dy, T, d, _size(shape.y_dt), "dy"), *_mat(dsum, T, d, res, "dsum"),
+        *_mat(sum, T, d, res, "sum"), _vec(w, d, _size(shape.w_dt), "w"), _vec(rstd, T, 4, "rstd"),
+        _vec(rng, 2, 8, "rng"), *_mat(dres, T, d, res, "dres"), *_mat(dx, T, d, _size(shape.x_dt), "dx"),
+        _vec(dw, d, 4, "dw"), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+
+
+def twell_dropout_add(shape: c_twell_norm_shape, x, residual, rng, y, stream=None) -> None:
+    """y = residual + dropout(x); with residual None also its own backward."""
+    T, d = shape.T, shape.d
+    _check(lib().twell_dropout_add(
+        shape, *_mat(x, T, d, _size(shape.x_dt), "x"), *_mat(residual, T, d, _size(shape.res_dt), "residual"),
+        _vec(rng, 2, 8, "rng"), *_mat(y, T, d, _size(shape.y_dt), "y"), _stream(stream)))
 
 
 def twell_status_string(st: int) -> str:

@@ -6,7 +6,7 @@
 
 namespace twell {
 
-enum { DT_F32 = 0, DT_BF16 = 1 };
+enum { DT_F32 = 0, DT_BF16 = 1, DT_MXFP8 = 2 };
 
 // Compute units of the current device (persistent grids are sized by it).
 inline int device_cus() {
@@ -235,5 +235,37 @@ hipError_t launch_zero_f32(float* p, int64_t n, hipStream_t s);
 hipError_t launch_dense_train(const void* x, const void* WgT, const void* bg, const void* WuT, const void* Wd,
                               const void* dY, int T, int d, int F, void* ws, int out_dt, void* y, float* dX,
                               float* dWgT, float* dWuT, float* dWd, float* dbg, hipStream_t s);
+
+// Records the calling thread's error text and returns st (twell_api.cpp).
+int set_error(int st, const char* fmt, ...);
+
+// ---------------------------------------------------------------- around the layer (block_norm.hip)
+
+// A [T][d] matrix of rows `ld` elements apart.
+struct RowMat {
+  void* p;
+  int64_t ld;
+  int dt;
+};
+struct NormArgs {
+  int T, d;
+  RowMat x, res, sum, y;     // forward; backward: x = dx, res = dsum, sum, y = dy, dres
+  RowMat dres;
+  const void* w;             // null: ones
+  int w_dt;
+  uint8_t* y_scale;          // MXFP8 y
+  float* rstd;
+  const float* rstd_in;      // backward
+  const uint64_t* rng;
+  uint32_t drop;             // 16-bit numbers below this are dropped; 0: no dropout
+  float keep_scale;          // 1 / (1 - drop / 65536), 0 where everything is dropped
+  float eps;
+  float* dw;
+  float* part;               // [norm_bwd_parts(T, d)][d] row sums of dw
+};
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
+int norm_bwd_parts(int T, int d);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_dropout_add(const NormArgs& a, hipStream_t s);
 
 }  // namespace twell

@@ -29,6 +29,18 @@ twell_status hip_status(hipError_t e, const char* what) {
   return fail(TWELL_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+}  // namespace
+
+int twell::set_error(int st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+namespace {
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -59,7 +59,11 @@ typedef enum {
   TWELL_EHIP = 4
 } twell_status;
 
-typedef enum { TWELL_F32 = 0, TWELL_BF16 = 1 } twell_dtype;
+/* TWELL_MXFP8 (activations of the calls that name it): 8-bit e4m3 values [T][d]
+ * (1 sign, 4 exponent and 3 mantissa bits, bias 7, largest value 448, no
+ * infinity) with one scale byte per 32 columns of a row, [T][ceil(d / 32)],
+ * each byte b standing for 2^(b - 127) and 255 for NaN. */
+typedef enum { TWELL_F32 = 0, TWELL_BF16 = 1, TWELL_MXFP8 = 2 } twell_dtype;
 
 /*
  * A [T x F] matrix of ReLU outputs in TwELL form (intellectnews.ru TwELL
@@ -501,6 +505,88 @@ twell_status twell_ffn_dense_bwd(const twell_ffn_shape *sh, const void *x, const
 twell_status twell_ffn_fwd_noalloc(const twell_ffn_shape *sh, const void *x, const void *WgT, const void *bg,
                                    const void *WuT, const void *Wd, void *y, twell_mat *saved_h,
                                    int32_t dense_row_threshold, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the layer: the residual stream, its norm and dropout
+ * ---------------------------------------------------------------------------
+ *
+ * Shape, dtypes and constants of the calls on [T][d] rows.  1 <= d <= 65536,
+ * T >= 0, any remainder.
+ *   x_dt    x, and in the backward dx                            (F32 or BF16)
+ *   res_dt  the residual stream: residual, sum, dsum, dres       (F32 or BF16)
+ *   y_dt    y, and in the backward dy   (F32 or BF16; MXFP8 in the norm forward)
+ *   w_dt    the norm's weights                                   (F32 or BF16)
+ *   eps     >= 0, added to the mean square
+ *   p       probability of a value being dropped, 0 <= p <= 1, taken to the
+ *           nearest multiple of 2^-16; 0 switches dropout off
+ * Each matrix argument is followed by its row stride in elements (>= d; ignored
+ * for T <= 1).  Pointers need the alignment of their elements only.
+ *
+ * Dropout takes its random numbers from a counter-based generator, so no mask
+ * is stored: Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011), key = rng[0], counter =
+ * (block, rng[1]), rng two 64-bit numbers in device memory (so a captured graph
+ * draws anew when they change).  Block t * ceil(d / 8) + c / 8 gives columns c
+ * .. c + 7 of row t eight 16-bit numbers (low half of word 0 first); a value is
+ * dropped (exactly 0, whatever it was) where its number is below 65536 p, and
+ * multiplied by 1 / (1 - p) otherwise.  The backward draws the same numbers.
+ */
+typedef struct {
+  int32_t T, d;
+  twell_dtype x_dt, res_dt, y_dt, w_dt;
+  float eps, p;
+} twell_norm_shape;
+
+/*
+ * twell_add_rmsnorm_fwd:
+ *     sum = residual + dropout(x)            (added in fp32, stored in res_dt)
+ *     y   = sum / sqrt(mean(sum^2) + eps) * w
+ *   residual   [T][d] or NULL (nothing is added)
+ *   w          [d] or NULL (ones)
+ *   rng        two uint64; may be NULL when p == 0
+ *   sum        [T][d], may be residual itself.  Required with a residual or
+ *              with p > 0, else it may be NULL; the norm is that of the stored
+ *              (rounded) sum, or of x where none is stored
+ *   y          [T][d]; in MXFP8 its codes, and y_scale [T][ceil(d / 32)] gets
+ *              the scales: the smallest power of two >= 2^-127 that holds the
+ *              32 values within +-448.  A group with an infinity or a NaN gets
+ *              scale 255 and NaN codes.  y_scale is NULL otherwise
+ *   rstd       [T] fp32, 1 / sqrt(mean(sum^2) + eps), or NULL
+ */
+twell_status twell_add_rmsnorm_fwd(const twell_norm_shape *sh, const void *x, int64_t ldx, const void *residual,
+                                   int64_t ldres, const void *w, const uint64_t *rng, void *sum, int64_t ldsum,
+                                   void *y, int64_t ldy, uint8_t *y_scale, float *rstd, hipStream_t stream);
+
+/* Workspace bytes for twell_add_rmsnorm_bwd (0 for an invalid shape). */
+size_t twell_add_rmsnorm_bwd_workspace(const twell_norm_shape *sh);
+
+/*
+ * twell_add_rmsnorm_bwd: the gradients of twell_add_rmsnorm_fwd for dy = dL/dy
+ * and dsum = dL/dsum (what reaches the sum by its other uses), from the stored
+ * sum and rstd.  With xh = sum * rstd and c = mean(dy * w * xh) of a row:
+ *     dres = rstd * (dy * w - xh * c) + dsum    (gradient of residual)
+ *     dx   = dropout(dres), the forward's mask  (gradient of x)
+ *     dw   = sum over the rows of dy * xh       (fp32, a fixed order)
+ *   dsum  [T][d] or NULL (zeros);  w, rng as in the forward
+ *   dres  [T][d] in res_dt, may be dsum itself; may be NULL when dx is given
+ *   dx    [T][d] in x_dt; may be NULL when dres is given
+ *   dw    [d] fp32 or NULL; zeros when T == 0
+ *   ws    twell_add_rmsnorm_bwd_workspace(sh) bytes, 16-byte aligned (used for
+ *         dw only)
+ */
+twell_status twell_add_rmsnorm_bwd(const twell_norm_shape *sh, const void *dy, int64_t lddy, const void *dsum,
+                                   int64_t lddsum, const void *sum, int64_t ldsum, const void *w, const float *rstd,
+                                   const uint64_t *rng, void *dres, int64_t lddres, void *dx, int64_t lddx,
+                                   float *dw, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * twell_dropout_add: y = residual + dropout(x), added in fp32; residual may be
+ * NULL, and y may be x or residual where dtype and stride agree.  Without a
+ * residual it is its own backward: dx = dropout(dy).  eps and w_dt are ignored.
+ */
+twell_status twell_dropout_add(const twell_norm_shape *sh, const void *x, int64_t ldx, const void *residual,
+                               int64_t ldres, const uint64_t *rng, void *y, int64_t ldy, hipStream_t stream);
 
 /* Static description of a status code. */
 const char *twell_status_string(twell_status st);

@@ -7,4 +7,7 @@ and the ``cpu_baseline`` leg of ``bench.py`` may import it; the product path
 imports the product.
 """
 from .twell_oracle import *  # noqa: F401,F403
-from .twell_oracle import __all__  # noqa: F401
+from .block_oracle import *  # noqa: F401,F403
+from . import block_oracle, twell_oracle
+
+__all__ = twell_oracle.__all__ + block_oracle.__all__
