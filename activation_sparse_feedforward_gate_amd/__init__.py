@@ -21,4 +21,5 @@ from ._lib import (  # noqa: F401
     twell_relu_ffn_fwd_bounded_workspace, twell_relu_ffn_fwd_bounded,
     TWELL_MXFP8, c_twell_norm_shape, norm_shape, twell_add_rmsnorm_fwd, twell_add_rmsnorm_bwd_workspace,
     twell_add_rmsnorm_bwd, twell_dropout_add,
+    TwellW4, c_twell_w4, twell_w4_matvec, twell_ffn_fwd_w4_workspace, twell_ffn_fwd_w4,
 )

@@ -47,6 +47,10 @@ class c_twell_norm_shape(ctypes.Structure):
                 ("y_dt", ctypes.c_int), ("w_dt", ctypes.c_int), ("eps", ctypes.c_float), ("p", ctypes.c_float)]
 
 
+class c_twell_w4(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -118,6 +122,11 @@ def lib() -> ctypes.CDLL:
         L.twell_add_rmsnorm_bwd.argtypes = [NS, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, sz,
                                             vp]
         L.twell_dropout_add.argtypes = [NS, vp, i64, vp, i64, vp, vp, i64, vp]
+        W4 = P(c_twell_w4)
+        L.twell_w4_matvec.argtypes = [i32, vp, ctypes.c_int, i64, vp, W4, vp, vp, ctypes.c_int, i64, vp]
+        L.twell_ffn_fwd_w4_workspace.argtypes = [P(c_twell_ffn_shape)]
+        L.twell_ffn_fwd_w4_workspace.restype = sz
+        L.twell_ffn_fwd_w4.argtypes = [P(c_twell_ffn_shape), vp, vp, W4, vp, W4, W4, vp, vp, sz, vp]
         L.twell_status_string.argtypes = [ctypes.c_int]
         L.twell_status_string.restype = ctypes.c_char_p
         L.twell_last_error.argtypes = []
@@ -129,7 +138,7 @@ def lib() -> ctypes.CDLL:
                      "twell_gate_pack",
                      "twell_sparse_up", "twell_sparse_down", "twell_ffn_fwd_noalloc", "twell_ffn_fwd_bounded",
                      "twell_ffn_fwd_compact", "twell_relu_ffn_fwd_bounded", "twell_add_rmsnorm_fwd",
-                     "twell_add_rmsnorm_bwd", "twell_dropout_add"):
+                     "twell_add_rmsnorm_bwd", "twell_dropout_add", "twell_w4_matvec", "twell_ffn_fwd_w4"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -534,6 +543,59 @@ def twell_dropout_add(shape: c_twell_norm_shape, x, residual, rng, y, stream=Non
     _check(lib().twell_dropout_add(
         shape, *_mat(x, T, d, _size(shape.x_dt), "x"), *_mat(residual, T, d, _size(shape.res_dt), "residual"),
         _vec(rng, 2, 8, "rng"), *_mat(y, T, d, _size(shape.y_dt), "y"), _stream(stream)))
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+@dataclass(frozen=True)
+class TwellW4:
+    """An MXFP4 weight matrix [N][K] (twell_w4 in include/twell.h): codes
+    [N][K / 2] and scales [N][K / 32], uint8 tensors."""
+    codes: object
+    scales: object
+
+    def __post_init__(self):
+        c, s = self.codes, self.scales
+        for t in (c, s):
+            if t.dim() != 2 or t.element_size() != 1 or not t.is_contiguous():
+                raise ValueError(f"TwellW4: expected a contiguous byte matrix, got {tuple(t.shape)} {t.dtype}")
+        if c.shape[0] != s.shape[0] or c.shape[1] != 16 * s.shape[1]:
+            raise ValueError(f"TwellW4: codes {tuple(c.shape)} do not go with scales {tuple(s.shape)}")
+
+    @property
+    def N(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def K(self) -> int:
+        return 2 * self.codes.shape[1]
+
+    def c(self) -> c_twell_w4:
+        return c_twell_w4(self.N, self.K, _ptr(self.codes), _ptr(self.scales))
+
+
+def twell_w4_matvec(x, x_scale, W: TwellW4, bias, y, stream=None) -> None:
+    """y = x . W^T + bias; x bf16, or MXFP8 with x_scale; y fp32 or bf16."""
+    T, N, K = x.shape[0], W.N, W.K
+    x_dt = TWELL_BF16 if x_scale is None else TWELL_MXFP8
+    px, ldx = _mat(x, T, K, _size(x_dt), "x")
+    py, ldy = _mat(y, T, N, _size(_dt(y.dtype)), "y")
+    _check(lib().twell_w4_matvec(T, px, x_dt, ldx, _vec(x_scale, T * (K // 32), 1, "x_scale"), W.c(),
+                                 _vec(bias, N, 2, "bias"), py, _dt(y.dtype), ldy, _stream(stream)))
+
+
+def twell_ffn_fwd_w4_workspace(shape: c_twell_ffn_shape) -> int:
+    return int(lib().twell_ffn_fwd_w4_workspace(shape))
+
+
+def twell_ffn_fwd_w4(shape: c_twell_ffn_shape, x, x_scale, Wg: TwellW4, bg, Wu: TwellW4, Wd: TwellW4, y, ws,
+                     stream=None) -> None:
+    """The layer on MXFP4 weights for few tokens; x bf16, or MXFP8 with x_scale."""
+    T, d, F = shape.T, shape.d, shape.F
+    _check(lib().twell_ffn_fwd_w4(
+        shape, _vec(x, T * d, _size(shape.in_dt), "x"), _vec(x_scale, T * (d // 32), 1, "x_scale"), Wg.c(),
+        _vec(bg, F, 2, "bg"), Wu.c(), Wd.c(), _vec(y, T * d, _size(shape.out_dt), "y"), _ptr(ws),
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
 
 
 def twell_status_string(st: int) -> str:

@@ -27,7 +27,7 @@ CFLAGS = [
     "-I", os.path.join(ROOT, "include"), "-Wall", "-Wno-unused-function",
 ]
 SOURCES = ["twell_api.cpp", "twell_gate.hip", "twell_sparse.hip", "twell_sparse_bf16.hip", "twell_union.hip", "twell_hybrid.hip", "dense_ffn.hip", "dense_train.hip", "twell_decode.hip", "twell_compact.hip",
-           "block_api.cpp", "block_norm.hip"]
+           "block_api.cpp", "block_norm.hip", "block_w4.hip"]
 
 
 def _compile(src: str) -> str:

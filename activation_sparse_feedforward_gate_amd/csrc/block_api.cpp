@@ -1,6 +1,6 @@
 // C-ABI entry points of the operators around the layer (residual sum, norm and
-// dropout): argument checks on the host, then kernel launches on the caller's
-// stream.  No allocation, no synchronisation.
+// dropout) and of those on 4-bit weights: argument checks on the host, then
+// kernel launches on the caller's stream.  No allocation, no synchronisation.
 #include <math.h>
 
 #include "../../include/twell.h"
@@ -65,6 +65,29 @@ NormArgs args_of(const twell_norm_shape* sh) {
   a.d = sh->d;
   a.eps = sh->eps;
   return a;
+}
+
+// One 4-bit weight matrix.
+twell_status w4(W4View* v, const twell_w4* W, const char* name) {
+  if (!W) return FAIL(TWELL_EINVAL, "%s is NULL", name);
+  if (W->N <= 0 || W->K <= 0) return FAIL(TWELL_EINVAL, "bad %s: N=%d K=%d", name, W->N, W->K);
+  if (W->K % 32) return FAIL(TWELL_EUNSUPPORTED, "%s: K=%d is not a multiple of 32", name, W->K);
+  if (!W->codes || !W->scales) return FAIL(TWELL_EINVAL, "%s: NULL array", name);
+  if ((uintptr_t)W->codes % 16) return FAIL(TWELL_EINVAL, "%s: codes are not 16-byte aligned", name);
+  v->code = W->codes;
+  v->scale = W->scales;
+  return TWELL_OK;
+}
+
+// Activations of a product with 4-bit weights.
+twell_status tokens(W4Args* a, const void* x, int x_dt, const uint8_t* x_scale) {
+  if (x_dt != TWELL_BF16 && x_dt != TWELL_MXFP8) return FAIL(TWELL_EINVAL, "x must be BF16 or MXFP8");
+  if ((x_dt == TWELL_MXFP8) != (x_scale != nullptr))
+    return FAIL(TWELL_EINVAL, "x_scale goes with an MXFP8 x and with no other");
+  if ((uintptr_t)x % dt_size(x_dt)) return FAIL(TWELL_EINVAL, "x is not aligned to its elements");
+  a->x = x;
+  a->x_scale = x_scale;
+  return TWELL_OK;
 }
 
 #define CHECK(call) \
@@ -139,6 +162,77 @@ twell_status twell_dropout_add(const twell_norm_shape* sh, const void* x, int64_
   CHECK(dropout(&a, sh, rng));
   if (!x || !y) return FAIL(TWELL_EINVAL, "NULL tensor argument");
   return hip_status(launch_dropout_add(a, stream), "dropout");
+}
+
+twell_status twell_w4_matvec(int32_t T, const void* x, twell_dtype x_dt, int64_t ldx, const uint8_t* x_scale,
+                             const twell_w4* W, const void* bias, void* y, twell_dtype y_dt, int64_t ldy,
+                             hipStream_t stream) {
+  W4Args a{};
+  if (T < 0) return FAIL(TWELL_EINVAL, "bad T=%d", T);
+  CHECK(w4(&a.W, W, "W"));
+  CHECK(tokens(&a, x, x_dt, x_scale));
+  if (!float_dt(y_dt)) return FAIL(TWELL_EINVAL, "y must be F32 or BF16");
+  if ((uintptr_t)y % dt_size(y_dt) || (uintptr_t)bias % 2)
+    return FAIL(TWELL_EINVAL, "y or bias is not aligned to its elements");
+  if (T == 0) return TWELL_OK;
+  if (!x || !y) return FAIL(TWELL_EINVAL, "NULL tensor argument");
+  if (T > 1 && (ldx < W->K || ldy < W->N))
+    return FAIL(TWELL_EINVAL, "row stride of x (%lld) or y (%lld) below K=%d or N=%d", (long long)ldx, (long long)ldy,
+                W->K, W->N);
+  a.T = T;
+  a.N = W->N;
+  a.K = W->K;
+  a.ldx = T > 1 ? ldx : W->K;
+  a.ldy = T > 1 ? ldy : W->N;
+  a.bias = (const uint16_t*)bias;
+  a.y = y;
+  a.y_bf16 = y_dt == TWELL_BF16;
+  return hip_status(launch_w4_matvec(a, stream), "4-bit product");
+}
+
+static twell_status check_ffn_w4_shape(const twell_ffn_shape* sh) {
+  if (!sh) return FAIL(TWELL_EINVAL, "shape is NULL");
+  if (sh->T < 0 || sh->d <= 0 || sh->F <= 0) return FAIL(TWELL_EINVAL, "bad shape T=%d d=%d F=%d", sh->T, sh->d, sh->F);
+  if ((sh->in_dt != TWELL_BF16 && sh->in_dt != TWELL_MXFP8) || !float_dt(sh->out_dt))
+    return FAIL(TWELL_EINVAL, "bad dtype (x BF16 or MXFP8, y F32 or BF16)");
+  if (sh->d % 64 || sh->F % 64) return FAIL(TWELL_EUNSUPPORTED, "d=%d and F=%d must be multiples of 64", sh->d, sh->F);
+  const int64_t lim = (int64_t)1 << 31;
+  if ((int64_t)sh->T * sh->d >= lim || (int64_t)sh->T * sh->F >= lim || (int64_t)sh->F * sh->d >= lim)
+    return FAIL(TWELL_EUNSUPPORTED, "T*d, T*F and F*d must be below 2^31");
+  return TWELL_OK;
+}
+
+size_t twell_ffn_fwd_w4_workspace(const twell_ffn_shape* sh) {
+  return check_ffn_w4_shape(sh) == TWELL_OK ? ffn_w4_ws_bytes(sh->T, sh->d, sh->F) : 0;
+}
+
+twell_status twell_ffn_fwd_w4(const twell_ffn_shape* sh, const void* x, const uint8_t* x_scale, const twell_w4* Wg,
+                              const void* bg, const twell_w4* Wu, const twell_w4* Wd, void* y, void* ws,
+                              size_t ws_bytes, hipStream_t stream) {
+  CHECK(check_ffn_w4_shape(sh));
+  if (sh->T == 0) return TWELL_OK;
+  W4Args a{};
+  CHECK(w4(&a.W, Wg, "Wg"));
+  CHECK(w4(&a.Wu, Wu, "Wu"));
+  CHECK(w4(&a.Wd, Wd, "Wd"));
+  for (const twell_w4* W : {Wg, Wu, Wd})
+    if (W->N != sh->F || W->K != sh->d)
+      return FAIL(TWELL_EINVAL, "a weight matrix is [%d][%d], not [F=%d][d=%d]", W->N, W->K, sh->F, sh->d);
+  CHECK(tokens(&a, x, sh->in_dt, x_scale));
+  if (!x || !y) return FAIL(TWELL_EINVAL, "NULL tensor argument");
+  if ((uintptr_t)y % dt_size(sh->out_dt) || (uintptr_t)bg % 2)
+    return FAIL(TWELL_EINVAL, "y or bg is not aligned to its elements");
+  const size_t need = ffn_w4_ws_bytes(sh->T, sh->d, sh->F);
+  if (!ws || ws_bytes < need) return FAIL(TWELL_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  if ((uintptr_t)ws % 16) return FAIL(TWELL_EINVAL, "the workspace must be 16-byte aligned");
+  a.T = sh->T;
+  a.N = sh->F;
+  a.K = sh->d;
+  a.ldx = a.ldy = sh->d;
+  a.bias = (const uint16_t*)bg;
+  a.y = y;
+  a.y_bf16 = sh->out_dt == TWELL_BF16;
+  return hip_status(launch_ffn_w4(a, ws, stream), "layer on 4-bit weights");
 }
 
 }  // extern "C"

@@ -268,4 +268,26 @@ int norm_bwd_parts(int T, int d);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_dropout_add(const NormArgs& a, hipStream_t s);
 
+// ---------------------------------------------------------------- 4-bit weights (block_w4.hip)
+
+struct W4View {
+  const uint8_t* code;       // [N][K / 2]
+  const uint8_t* scale;      // [N][K / 32]
+};
+struct W4Args {
+  int T, N, K;               // the layer: N = F, K = d
+  const void* x;             // [T][K] bf16 or e4m3
+  int64_t ldx;
+  const uint8_t* x_scale;    // [T][K / 32], null for bf16
+  W4View W, Wu, Wd;
+  const uint16_t* bias;      // [N] bf16 or null
+  void* y;
+  int64_t ldy;
+  int y_bf16;
+  float* act;                // the layer: a = h * u [T][F]
+};
+hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s);
+size_t ffn_w4_ws_bytes(int T, int d, int F);
+hipError_t launch_ffn_w4(W4Args a, void* ws, hipStream_t s);
+
 }  // namespace twell

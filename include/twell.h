@@ -588,6 +588,56 @@ twell_status twell_add_rmsnorm_bwd(const twell_norm_shape *sh, const void *dy, i
 twell_status twell_dropout_add(const twell_norm_shape *sh, const void *x, int64_t ldx, const void *residual,
                                int64_t ldres, const uint64_t *rng, void *y, int64_t ldy, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Serving on 4-bit weights
+ * ---------------------------------------------------------------------------
+ *
+ * A weight matrix [N][K] in MXFP4 (K % 32 == 0): e2m1 values (1 sign, 2
+ * exponent and 1 mantissa bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale per 32
+ * columns of a row.
+ *   codes   uint8 [N][K / 2]   two values a byte, the even column in the low
+ *                              four bits; 16-byte aligned
+ *   scales  uint8 [N][K / 32]  byte b stands for 2^(b - 127), 255 for NaN
+ */
+typedef struct {
+  int32_t N, K;
+  const uint8_t *codes;
+  const uint8_t *scales;
+} twell_w4;
+
+/*
+ * twell_w4_matvec: y = x . W^T + bias for a few tokens, accumulated in fp32;
+ * any T >= 0 and N >= 1.  The weights are read once per 64 tokens.
+ *   x        [T][K], rows ldx elements apart, x_dt BF16, or MXFP8 with
+ *            x_scale [T][K / 32] (NULL for BF16): what twell_add_rmsnorm_fwd
+ *            writes
+ *   bias     [N] BF16 or NULL
+ *   y        [T][N], rows ldy elements apart, y_dt F32 or BF16
+ * Strides are ignored for T <= 1; x and y need the alignment of their elements.
+ */
+twell_status twell_w4_matvec(int32_t T, const void *x, twell_dtype x_dt, int64_t ldx, const uint8_t *x_scale,
+                             const twell_w4 *W, const void *bias, void *y, twell_dtype y_dt, int64_t ldy,
+                             hipStream_t stream);
+
+/* Workspace bytes for twell_ffn_fwd_w4 (0 for an invalid shape or T == 0). */
+size_t twell_ffn_fwd_w4_workspace(const twell_ffn_shape *sh);
+
+/*
+ * twell_ffn_fwd_w4: the layer of twell_ffn_fwd on MXFP4 weights Wg, Wu and Wd
+ * (each N = F, K = d), for the few tokens of a serving step: the gate reads Wg
+ * once per 64 tokens, and of Wu and Wd only the rows of neurons that fire
+ * (g > 0 in fp32) are read.  in_dt BF16 or MXFP8 (of x), out_dt F32 or BF16;
+ * products and h, u, a are accumulated and kept in fp32.
+ *   x        [T][d]; x_scale [T][d / 32] for MXFP8, NULL for BF16
+ *   bg       [F] BF16 or NULL
+ *   y        [T][d]
+ *   ws       twell_ffn_fwd_w4_workspace(sh) bytes, 16-byte aligned
+ */
+twell_status twell_ffn_fwd_w4(const twell_ffn_shape *sh, const void *x, const uint8_t *x_scale, const twell_w4 *Wg,
+                              const void *bg, const twell_w4 *Wu, const twell_w4 *Wd, void *y, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+
 /* Static description of a status code. */
 const char *twell_status_string(twell_status st);
 /* Thread-local description of the last error returned on this thread. */
