@@ -1,7 +1,12 @@
 // The residual stream around the layer: sum = residual + dropout(x) and its
 // root-mean-square norm, forward and backward, and dropout with a residual
-// alone.  All of it is a pass over [T][d] rows, bound by memory: 6 to 12
-// operations a value.
+// alone.  All of it is one pass over [T][d] rows, bound by memory: 6 to 12
+// operations a value beside the random numbers.
+//
+// Rows are held in registers between the row's sum and its use, so every byte
+// is read and written once.  LPR lanes take a row, CH chunks of eight columns
+// each; LPR <= 64 needs no barrier, and 256 / LPR rows share a workgroup where
+// LPR < 256.
 #include "internal.hpp"
 #include "row_ops.hpp"
 
@@ -9,29 +14,33 @@ namespace twell {
 
 namespace {
 
-constexpr int NTH = 256;
-
 struct mx8_t { static constexpr int size = 1; };   // MXFP8 y
 
-__device__ __forceinline__ float block_sum(float v, float* sh) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
+// Sum over the LPR lanes of a row; every lane gets it.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* sh) {
 #pragma unroll
-  for (int i = 0; i < NTH / 64; ++i) s += sh[i];
-  __syncthreads();
-  return s;
+  for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1) v += __shfl_xor(v, o);
+  if constexpr (LPR > 64) {
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const float* mine = sh + threadIdx.x / LPR * (LPR / 64);
+    v = mine[0];
+#pragma unroll
+    for (int i = 1; i < LPR / 64; ++i) v += mine[i];
+    __syncthreads();
+  }
+  return v;
 }
 
-__device__ __forceinline__ void load_w(const NormArgs& a, int c, int n, float w[8]) {
+__device__ __forceinline__ void load_w(const NormArgs& a, int c, float w[8]) {
   if (!a.w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f;
   } else if (a.w_dt == DT_F32) {
-    load8<f32_t>(a.w, c, n, w);
+    chunk_values(load_chunk<f32_t>(a.w, c, a.d), c, a.d, w);
   } else {
-    load8<bf16_t>(a.w, c, n, w);
+    chunk_values(load_chunk<bf16_t>(a.w, c, a.d), c, a.d, w);
   }
 }
 
@@ -69,72 +78,193 @@ __device__ __forceinline__ void mx_store(const NormArgs& a, int64_t t, int c, in
   uint32_t code[2], byte;
   mx_encode(v, code, byte);
   char* p = (char*)a.y.p + t * a.y.ld + c;
-  if (n == 8) {
+  if (n >= 8) {
     memcpy(p, code, 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (i < n) p[i] = (char)(code[i >> 2] >> (8 * (i & 3)));
   }
   if ((c & 31) == 0 && n > 0) a.y_scale[t * ((a.d + 31) / 32) + (c >> 5)] = (uint8_t)byte;
 }
 
+constexpr int threads_of(int lpr) { return lpr < 256 ? 256 : lpr; }
+
 }  // namespace
 
-// One workgroup a row; the second pass reads the stored sum back.
-template <class X, class R, class Y>
-__global__ __launch_bounds__(NTH) void norm_fwd_kernel(NormArgs a) {
-  __shared__ float sh[NTH / 64];
+template <class X, class R, class Y, int LPR, int CH>
+__global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
+  __shared__ float sh[threads_of(LPR) / 64];
+  constexpr int RPB = threads_of(LPR) / LPR;
+  const int lane = threadIdx.x % LPR;
   Philox g{};
   if (a.drop) g.load(a.rng);
   const int nb = (a.d + 7) / 8;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  // A row past the end is computed as the last one and not stored (its lanes
+  // take part in the shuffles).
+  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB) {
+    int64_t t = t0 + threadIdx.x / LPR;
+    const bool live = t < a.T;
+    t = live ? t : a.T - 1;
     const char* xr = row_of<X>(a.x, t);
-    const char* rr = a.res.p ? row_of<R>(a.res, t) : nullptr;
-    char* sr = a.sum.p ? row_of<R>(a.sum, t) : nullptr;
-    float sq = 0.f;
-    for (int c = threadIdx.x * 8; c < a.d; c += NTH * 8) {
-      const int n = min(a.d - c, 8);
-      float v[8], r[8];
-      load8<X>(xr, c, n, v);
-      if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, v);
-      if (rr) {
-        load8<R>(rr, c, n, r);
+    const char* rr = row_of<R>(a.res, t);
+    char* sr = row_of<R>(a.sum, t);
+    Raw8<X> xv[CH];
+    Raw8<R> rv[CH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-      }
-      if (sr) {
-        store8<R>(sr, c, n, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = stored<R>(v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) sq += v[i] * v[i];
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * LPR + lane) * 8;
+      xv[k] = load_chunk<X>(xr, c, a.d);
     }
-    const float rstd = 1.f / sqrtf(block_sum(sq, sh) / (float)a.d + a.eps);
-    if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
-    for (int c0 = 0; c0 < a.d; c0 += NTH * 8) {
-      const int c = c0 + threadIdx.x * 8, n = max(0, min(a.d - c, 8));
-      float v[8] = {}, w[8] = {};
-      if (n > 0) {
-        if (sr) load8<R>(sr, c, n, v);
-        else load8<X>(xr, c, n, v);
-        load_w(a, c, n, w);
-      }
+    if (a.res.p) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] * rstd * w[i] : 0.f;
-      if constexpr (Y::size == 1) mx_store(a, t, c, n, v);
-      else if (n > 0) store8<Y>(row_of<Y>(a.y, t), c, n, v);
+      for (int k = 0; k < CH; ++k) {
+        const int c = (k * LPR + lane) * 8;
+        rv[k] = load_chunk<R>(rr, c, a.d);
+      }
+    }
+    float v[CH][8], sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * LPR + lane) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+      if (c < a.d) {
+        chunk_values(xv[k], c, a.d, v[k]);
+        if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, v[k]);
+        if (a.res.p) {
+          float r[8];
+          chunk_values(rv[k], c, a.d, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] += r[i];
+        }
+        if (a.sum.p) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] = stored<R>(v[k][i]);
+          if (live) store8<R>(sr, c, a.d - c, v[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq += v[k][i] * v[k][i];     // columns past d are 0
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, sh) / (float)a.d + a.eps);
+    if (live && lane == 0 && a.rstd) a.rstd[t] = rstd;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * LPR + lane) * 8;
+      float w[8];
+      if (c < a.d) {
+        load_w(a, c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * rstd * w[i];
+      }
+      if constexpr (Y::size == 1) mx_store(a, t, c, live ? a.d - c : 0, v[k]);
+      else if (live && c < a.d) store8<Y>(row_of<Y>(a.y, t), c, a.d - c, v[k]);
     }
   }
 }
 
 // The rows are dealt out to gridDim.x workgroups; each leaves its rows' part
 // of dw in its row of `part`.
+template <class Y, class R, class X, int LPR, int CH>
+__global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int NTH = threads_of(LPR), RPB = NTH / LPR;
+  __shared__ float sh[RPB > 1 ? 8 * NTH : NTH / 64];
+  const int lane = threadIdx.x % LPR;
+  Philox g{};
+  if (a.drop) g.load(a.rng);
+  const int nb = (a.d + 7) / 8;
+  float dw[CH][8] = {};
+  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB) {
+    int64_t t = t0 + threadIdx.x / LPR;
+    const bool live = t < a.T;
+    t = live ? t : a.T - 1;
+    const char* yr = row_of<Y>(a.y, t);
+    const char* sr = row_of<R>(a.sum, t);
+    Raw8<Y> yv[CH];
+    Raw8<R> sv[CH], ds[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * LPR + lane) * 8;
+      yv[k] = load_chunk<Y>(yr, c, a.d);
+      sv[k] = load_chunk<R>(sr, c, a.d);
+    }
+    if (a.res.p) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int c = (k * LPR + lane) * 8;
+        ds[k] = load_chunk<R>(row_of<R>(a.res, t), c, a.d);
+      }
+    }
+    const float rstd = a.rstd_in[t];
+    float dot = 0.f;
+    float gy[CH][8];                                           // dy * w
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * LPR + lane) * 8;
+      if (c < a.d) {
+        float v[8], w[8];
+        chunk_values(yv[k], c, a.d, gy[k]);
+        chunk_values(sv[k], c, a.d, v);
+        load_w(a, c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {                          // columns past d: 0 * 0
+          const float xh = v[i] * rstd;
+          if (live) dw[k][i] += gy[k][i] * xh;
+          gy[k][i] *= w[i];
+          dot += gy[k][i] * xh;
+        }
+      }
+    }
+    const float cm = row_sum<LPR>(dot, sh) / (float)a.d;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int c = (k * LPR + lane) * 8, n = a.d - c;
+        if (n > 0) {
+          float v[8], o[8] = {};
+          chunk_values(sv[k], c, a.d, v);
+          if (a.res.p) chunk_values(ds[k], c, a.d, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += rstd * (gy[k][i] - v[i] * rstd * cm);
+          if (a.dres.p) store8<R>(row_of<R>(a.dres, t), c, n, o);
+          if (a.x.p) {
+            if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, o);
+            store8<X>(row_of<X>(a.x, t), c, n, o);
+          }
+        }
+      }
+    }
+  }
+  if (!a.dw) return;
+  float* part = a.part + (int64_t)blockIdx.x * a.d;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sh[i * NTH + threadIdx.x] = dw[k][i];
+      __syncthreads();
+      if (threadIdx.x < LPR) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw[k][i] = sh[i * NTH + threadIdx.x];
+#pragma unroll
+          for (int r = 1; r < RPB; ++r) dw[k][i] += sh[i * NTH + r * LPR + threadIdx.x];
+        }
+      }
+    }
+    const int c = (k * LPR + lane) * 8;
+    if (threadIdx.x < LPR && c < a.d) store8<f32_t>(part, c, a.d - c, dw[k]);
+  }
+}
+
+// The backward of wide rows (their values, gradients and part of dw do not fit
+// the registers): two passes over the row, dw's part kept in memory.
+constexpr int WIDE = 1024;
 template <class Y, class R, class X>
-__global__ __launch_bounds__(NTH) void norm_bwd_kernel(NormArgs a) {
-  __shared__ float sh[NTH / 64];
+__global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormArgs a) {
+  __shared__ float sh[WIDE / 64];
   Philox g{};
   if (a.drop) g.load(a.rng);
   const int nb = (a.d + 7) / 8;
@@ -144,30 +274,32 @@ __global__ __launch_bounds__(NTH) void norm_bwd_kernel(NormArgs a) {
     const char* sr = row_of<R>(a.sum, t);
     const float rstd = a.rstd_in[t];
     float dot = 0.f;
-    for (int c = threadIdx.x * 8; c < a.d; c += NTH * 8) {
+    for (int c = threadIdx.x * 8; c < a.d; c += WIDE * 8) {
       const int n = min(a.d - c, 8);
       float dy[8], v[8], w[8];
       load8<Y>(yr, c, n, dy);
       load8<R>(sr, c, n, v);
-      load_w(a, c, n, w);
+      load_w(a, c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < n) dot += dy[i] * w[i] * (v[i] * rstd);
     }
-    const float cm = block_sum(dot, sh) / (float)a.d;
-    for (int c = threadIdx.x * 8; c < a.d; c += NTH * 8) {
+    const float cm = row_sum<WIDE>(dot, sh) / (float)a.d;
+    for (int c = threadIdx.x * 8; c < a.d; c += WIDE * 8) {
       const int n = min(a.d - c, 8);
-      float dy[8], v[8], w[8], ds[8] = {};
+      float dy[8], v[8], w[8], ds[8] = {}, p[8] = {};
       load8<Y>(yr, c, n, dy);
       load8<R>(sr, c, n, v);
-      load_w(a, c, n, w);
+      load_w(a, c, w);
       if (a.res.p) load8<R>(row_of<R>(a.res, t), c, n, ds);
+      if (part && t != blockIdx.x) load8<f32_t>(part, c, n, p);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xh = v[i] * rstd;
-        if (part && i < n) part[c + i] = (t == blockIdx.x ? 0.f : part[c + i]) + dy[i] * xh;
+        p[i] += dy[i] * xh;
         ds[i] += rstd * (dy[i] * w[i] - xh * cm);
       }
+      if (part) store8<f32_t>(part, c, n, p);
       if (a.dres.p) store8<R>(row_of<R>(a.dres, t), c, n, ds);
       if (a.x.p) {
         if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, ds);
@@ -177,28 +309,43 @@ __global__ __launch_bounds__(NTH) void norm_bwd_kernel(NormArgs a) {
   }
 }
 
-// dw = the parts, added in a fixed order.
-__global__ __launch_bounds__(NTH) void norm_dw_kernel(const float* part, int parts, int d, float* dw) {
-  const int c = blockIdx.x * NTH + threadIdx.x;
-  if (c >= d) return;
+// dw = the parts, added in a fixed order: 32 columns a workgroup, 32 threads a
+// column.
+constexpr int DW_COLS = 32, DW_ROWS = 32;
+__global__ __launch_bounds__(DW_COLS * DW_ROWS) void norm_dw_kernel(const float* part, int parts, int d, float* dw) {
+  __shared__ float sh[DW_ROWS][DW_COLS + 1];
+  const int x = threadIdx.x % DW_COLS, y = threadIdx.x / DW_COLS, c = blockIdx.x * DW_COLS + x;
   float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += part[(int64_t)i * d + c];
-  dw[c] = s;
+  if (c < d) {
+#pragma unroll 4
+    for (int i = y; i < parts; i += DW_ROWS) s += part[(int64_t)i * d + c];
+  }
+  sh[y][x] = s;
+  __syncthreads();
+  if (y == 0 && c < d) {
+    for (int i = 1; i < DW_ROWS; ++i) s += sh[i][x];
+    dw[c] = s;
+  }
 }
 
+// rpb rows a workgroup where a row has fewer than 256 chunks of eight columns,
+// otherwise one.
+constexpr int DROP_NTH = 256;
 template <class X, class R, class Y>
-__global__ __launch_bounds__(NTH) void dropout_add_kernel(NormArgs a) {
+__global__ __launch_bounds__(DROP_NTH) void dropout_add_kernel(NormArgs a, int rpb) {
   Philox g{};
   if (a.drop) g.load(a.rng);
   const int nb = (a.d + 7) / 8;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
-    for (int c = threadIdx.x * 8; c < a.d; c += NTH * 8) {
-      const int n = min(a.d - c, 8);
-      float v[8], r[8];
+  const int row = rpb > 1 ? threadIdx.x / nb : 0;
+  if (row >= rpb) return;
+  for (int64_t t = (int64_t)blockIdx.x * rpb + row; t < a.T; t += (int64_t)gridDim.x * rpb)
+    for (int b = rpb > 1 ? threadIdx.x % nb : threadIdx.x; b < nb; b += DROP_NTH) {
+      const int c = 8 * b, n = a.d - c;
+      float v[8], r[8] = {};
       load8<X>(row_of<X>(a.x, t), c, n, v);
-      if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, v);
+      if (a.res.p) load8<R>(row_of<R>(a.res, t), c, n, r);
+      if (a.drop) dropout8(g, t * nb + b, a.drop, a.keep_scale, v);
       if (a.res.p) {
-        load8<R>(row_of<R>(a.res, t), c, n, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += r[i];
       }
@@ -220,37 +367,102 @@ void with_types(int a, int b, int c, F f) {
 
 constexpr int64_t ROW_GRID = 1 << 20;    // workgroups of a launch; more rows are walked in a loop
 
+// Lanes per row and chunks per lane.
+template <int LPR_, int CH_>
+struct Cfg {
+  static constexpr int LPR = LPR_, CH = CH_, RPB = threads_of(LPR_) / LPR_;
+};
+
+// Few chunks per lane and few idle lanes: two or three chunks in flight per lane
+// fill the memory pipe, more cost registers and so waves.  32768 rows of 2304
+// (fp32 x, bf16 rest, dropout): <128, 3> 137 us (5.5 TB/s), <256, 2> 144, <64, 5>
+// 166, <64, 8> 273.  Up to 512 rows the time is one row's latency and one chunk
+// a lane is fastest: 1 row of 2304 to MXFP8, <512, 1> 3.5 us, <256, 2> 4.2, <128, 3>
+// 5.2; 1024 rows, 7.7, 6.5 and 6.9.
+template <class F>
+void with_fwd_cfg(int T, int d, F f) {
+  if (T <= 512 && d > 512) {
+    if (d <= 2048) return f(Cfg<256, 1>{});
+    if (d <= 4096) return f(Cfg<512, 1>{});
+  }
+  if (d <= 128) return f(Cfg<16, 1>{});
+  if (d <= 256) return f(Cfg<32, 1>{});
+  if (d <= 512) return f(Cfg<64, 1>{});
+  if (d <= 1024) return f(Cfg<128, 1>{});
+  if (d <= 2048) return f(Cfg<128, 2>{});
+  if (d <= 2560) return f(Cfg<128, 3>{});
+  if (d <= 4096) return f(Cfg<256, 2>{});
+  if (d <= 8192) return f(Cfg<512, 2>{});
+  if (d <= 16384) return f(Cfg<1024, 2>{});
+  if (d <= 32768) return f(Cfg<1024, 4>{});
+  return f(Cfg<1024, 8>{});
+}
+
+// The backward holds two inputs, the gradient and its part of dw per chunk, and
+// its workgroups (the second argument: as many as 256 CUs hold at once) walk
+// the rows, so that a part of dw is written once.  32768 rows of 2304: <512, 1>
+// 183 us (4.9 TB/s), <128, 3> 183, <256, 2> 189, <64, 5> 248; with twice the
+// workgroups 188, 187, 196, 252.
+constexpr int BWD_MAX_D = 16384;
+template <class F>
+void with_bwd_cfg(int d, F f) {
+  if (d <= 128) return f(Cfg<16, 1>{}, 1280);
+  if (d <= 256) return f(Cfg<32, 1>{}, 1280);
+  if (d <= 512) return f(Cfg<64, 1>{}, 1280);
+  if (d <= 1024) return f(Cfg<128, 1>{}, 1024);
+  if (d <= 2048) return f(Cfg<128, 2>{}, 768);
+  if (d <= 4096) return f(Cfg<512, 1>{}, 512);
+  if (d <= 8192) return f(Cfg<1024, 1>{}, 256);
+  return f(Cfg<1024, 2>{}, 256);
+}
+
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.T < ROW_GRID ? a.T : ROW_GRID));
   with_types(a.x.dt, a.res.dt, a.y.dt == DT_MXFP8 ? DT_F32 : a.y.dt, [&](auto x, auto r, auto y) {
     using X = decltype(x); using R = decltype(r); using Y = decltype(y);
-    if (a.y.dt == DT_MXFP8) norm_fwd_kernel<X, R, mx8_t><<<grid, NTH, 0, s>>>(a);
-    else norm_fwd_kernel<X, R, Y><<<grid, NTH, 0, s>>>(a);
+    with_fwd_cfg(a.T, a.d, [&](auto c) {
+      using C = decltype(c);
+      const int64_t blocks = ((int64_t)a.T + C::RPB - 1) / C::RPB;
+      const dim3 grid((unsigned)(blocks < ROW_GRID ? blocks : ROW_GRID));
+      if (a.y.dt == DT_MXFP8) norm_fwd_kernel<X, R, mx8_t, C::LPR, C::CH><<<grid, threads_of(C::LPR), 0, s>>>(a);
+      else norm_fwd_kernel<X, R, Y, C::LPR, C::CH><<<grid, threads_of(C::LPR), 0, s>>>(a);
+    });
   });
   return hipGetLastError();
 }
 
 int norm_bwd_parts(int T, int d) {
-  (void)d;
-  return T < 1024 ? T : 1024;
+  int64_t blocks = T, most = 512;
+  if (d <= BWD_MAX_D)
+    with_bwd_cfg(d, [&](auto c, int n) {
+      blocks = ((int64_t)T + c.RPB - 1) / c.RPB;
+      most = n;
+    });
+  return (int)(blocks < most ? blocks : most);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   const int parts = norm_bwd_parts(a.T, a.d);
   if (a.T > 0)
     with_types(a.y.dt, a.res.dt, a.x.dt, [&](auto y, auto r, auto x) {
-      norm_bwd_kernel<decltype(y), decltype(r), decltype(x)><<<dim3(parts), NTH, 0, s>>>(a);
+      using Y = decltype(y); using R = decltype(r); using X = decltype(x);
+      if (a.d > BWD_MAX_D) return norm_bwd_wide_kernel<Y, R, X><<<dim3(parts), WIDE, 0, s>>>(a);
+      with_bwd_cfg(a.d, [&](auto c, int) {
+        using C = decltype(c);
+        norm_bwd_kernel<Y, R, X, C::LPR, C::CH><<<dim3(parts), threads_of(C::LPR), 0, s>>>(a);
+      });
     });
-  if (a.dw) norm_dw_kernel<<<dim3((a.d + NTH - 1) / NTH), NTH, 0, s>>>(a.part, parts, a.d, a.dw);
+  if (a.dw) norm_dw_kernel<<<dim3((a.d + DW_COLS - 1) / DW_COLS), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
   return hipGetLastError();
 }
 
 hipError_t launch_dropout_add(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.T < ROW_GRID ? a.T : ROW_GRID));
+  const int nb = (a.d + 7) / 8, rpb = nb < DROP_NTH ? DROP_NTH / nb : 1;
+  const int64_t blocks = ((int64_t)a.T + rpb - 1) / rpb;
+  const dim3 grid((unsigned)(blocks < ROW_GRID ? blocks : ROW_GRID));
   with_types(a.x.dt, a.res.dt, a.y.dt, [&](auto x, auto r, auto y) {
-    dropout_add_kernel<decltype(x), decltype(r), decltype(y)><<<grid, NTH, 0, s>>>(a);
+    dropout_add_kernel<decltype(x), decltype(r), decltype(y)><<<grid, DROP_NTH, 0, s>>>(a, rpb);
   });
   return hipGetLastError();
 }

@@ -15,41 +15,83 @@ __device__ __forceinline__ uint32_t bf16_round(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// n valid (0..8) of the eight columns from element c0 of a row: one or two
-// 16-byte loads for a whole chunk, single loads at the row's ragged end.  The
-// 16-byte accesses need no more than the elements' alignment (global memory is
-// in unaligned access mode), so any row stride takes them.
+// Eight columns of a row as loaded, and their fp32 values.
 template <class E>
-__device__ __forceinline__ void load8(const void* row, int c0, int n, float v[8]) {
-  const char* p = (const char*)row + (int64_t)c0 * E::size;
-  if (n == 8) {
-    if constexpr (E::size == 4) {
-      memcpy(v, __builtin_assume_aligned(p, 4), 32);
-    } else {
-      uint32_t u[4];
-      memcpy(u, __builtin_assume_aligned(p, 2), 16);
+struct Raw8;
+template <>
+struct Raw8<f32_t> {
+  uint32_t u[8];
+  __device__ __forceinline__ void values(float v[8]) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(u[i]);
-        v[2 * i + 1] = bf16_hi(u[i]);
-      }
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+  }
+};
+template <>
+struct Raw8<bf16_t> {
+  uint32_t u[4];
+  __device__ __forceinline__ void values(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(u[i]);
+      v[2 * i + 1] = bf16_hi(u[i]);
     }
+  }
+};
+
+// n valid (0..8, the others 0) of the eight columns from element c0 of a row:
+// one or two 16-byte loads for a whole chunk, single loads at the row's ragged
+// end.  The 16-byte accesses need no more than the elements' alignment (global
+// memory is in unaligned access mode), so any row stride takes them.
+template <class E>
+__device__ __forceinline__ Raw8<E> load_raw(const void* row, int c0, int n) {
+  Raw8<E> r;
+  const char* p = (const char*)row + (int64_t)c0 * E::size;
+  if (n >= 8) {
+    memcpy(r.u, __builtin_assume_aligned(p, E::size), sizeof(r.u));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.f;
+    for (uint32_t& u : r.u) u = 0;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
       if (i < n) {
-        if constexpr (E::size == 4) v[i] = ((const float*)p)[i];
-        else v[i] = bf16_to_f32(((const uint16_t*)p)[i]);
+        if constexpr (E::size == 4) r.u[i] = ((const uint32_t*)p)[i];
+        else r.u[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
       }
-    }
+  }
+  return r;
+}
+
+template <class E>
+__device__ __forceinline__ void load8(const void* row, int c0, int n, float v[8]) {
+  load_raw<E>(row, c0, n).values(v);
+}
+
+// The same for a kernel that issues the loads of many chunks before it uses
+// them: one whole load at min(c, d - 8), with no branch (a branch per chunk ends
+// in a wait for its loads), and the ragged last chunk of a row is shifted into
+// place when it is used.  Chunks past the row's end load its last columns and
+// are not to be used.
+template <class E>
+__device__ __forceinline__ Raw8<E> load_chunk(const void* row, int c, int d) {
+  if (d < 8) return load_raw<E>(row, c, d - c);      // one chunk in all
+  return load_raw<E>(row, min(c, d - 8), 8);
+}
+template <class E>
+__device__ __forceinline__ void chunk_values(const Raw8<E>& r, int c, int d, float v[8]) {
+  r.values(v);
+  if (d % 8 && d > 8) {
+    const int miss = c - min(c, d - 8);
+#pragma unroll
+    for (int k = 4; k; k >>= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = miss & k ? (i + k < 8 ? v[i + k] : 0.f) : v[i];
   }
 }
 
 template <class E>
 __device__ __forceinline__ void store8(void* row, int c0, int n, const float v[8]) {
   char* p = (char*)row + (int64_t)c0 * E::size;
-  if (n == 8) {
+  if (n >= 8) {
     if constexpr (E::size == 4) {
       memcpy(__builtin_assume_aligned(p, 4), v, 32);
     } else {

@@ -91,6 +91,22 @@ def test_norm_fwd_sizes(torch, tw, T, d):
         check_norm(values(y), values(rstd), values(s), values(w)[0], HALF[yd])
 
 
+@pytest.mark.parametrize("T,d", [(515, 40), (601, 129), (515, 257), (514, 520), (601, 1001), (513, 1032), (515, 1999),
+                                 (514, 2304), (513, 2560), (515, 2567), (513, 4090), (514, 5001), (513, 9000),
+                                 (513, 17000)])
+def test_norm_fwd_many_rows(torch, tw, T, d):
+    """Widths of every lane layout with more rows than the latency-bound calls
+    have, the last workgroup partly filled."""
+    test_norm_fwd_sizes(torch, tw, T, d)
+
+
+@pytest.mark.parametrize("T,d", [(1283 * 16, 24), (1281 * 8 + 3, 200), (1281 * 4 + 1, 300), (1024 * 2 + 3, 1001),
+                                 (768 * 2 + 1, 1999), (1030, 2304), (515, 4100), (513, 9000), (1025, 16500)])
+def test_norm_bwd_many_rows(torch, tw, T, d):
+    """More rows than one round of the workgroups takes, at every lane layout."""
+    bwd_case(torch, tw, T, d, "f32", "bf16", "bf16", 0.1)
+
+
 @pytest.mark.parametrize("xd", ["f32", "bf16"])
 @pytest.mark.parametrize("rd", ["f32", "bf16"])
 @pytest.mark.parametrize("yd", ["f32", "bf16", "mx8"])
