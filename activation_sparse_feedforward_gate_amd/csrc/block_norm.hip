@@ -340,16 +340,19 @@ __global__ __launch_bounds__(DROP_NTH) void dropout_add_kernel(NormArgs a, int r
   if (row >= rpb) return;
   for (int64_t t = (int64_t)blockIdx.x * rpb + row; t < a.T; t += (int64_t)gridDim.x * rpb)
     for (int b = rpb > 1 ? threadIdx.x % nb : threadIdx.x; b < nb; b += DROP_NTH) {
-      const int c = 8 * b, n = a.d - c;
-      float v[8], r[8] = {};
-      load8<X>(row_of<X>(a.x, t), c, n, v);
-      if (a.res.p) load8<R>(row_of<R>(a.res, t), c, n, r);
+      const int c = 8 * b;
+      float v[8], r[8];
+      const Raw8<X> xv = load_chunk<X>(row_of<X>(a.x, t), c, a.d);
+      Raw8<R> rv;
+      if (a.res.p) rv = load_chunk<R>(row_of<R>(a.res, t), c, a.d);
+      chunk_values(xv, c, a.d, v);
       if (a.drop) dropout8(g, t * nb + b, a.drop, a.keep_scale, v);
       if (a.res.p) {
+        chunk_values(rv, c, a.d, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += r[i];
       }
-      store8<Y>(row_of<Y>(a.y, t), c, n, v);
+      store8<Y>(row_of<Y>(a.y, t), c, a.d - c, v);
     }
 }
 
