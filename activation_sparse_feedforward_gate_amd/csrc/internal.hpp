@@ -284,7 +284,8 @@ struct W4Args {
   void* y;
   int64_t ldy;
   int y_bf16;
-  float* act;                // the layer: a = h * u [T][F]
+  float* act;                // the layer: a = h * u [T][F], written where the pair fires
+  uint16_t* mask;            // the layer: bit n of row t set where it fires [T][F / 16]
 };
 hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s);
 size_t ffn_w4_ws_bytes(int T, int d, int F);
