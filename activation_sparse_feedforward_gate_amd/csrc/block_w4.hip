@@ -2,16 +2,25 @@
 //
 // y = x . W^T reads N K / 2 bytes of codes for 2 T N K operations: at up to 64
 // tokens it is bound by the weights' bytes, and by latency where they are few.
-// So the weights go from memory straight into the matrix instructions' operand
-// registers: a lane's 32 consecutive K of one row are one block, 16 bytes of
-// codes and one scale byte.  The tokens are the other operand, read from cache
-// in fragments too; no tile goes through LDS.  The waves of a workgroup split K
-// between them and add their sums in LDS in a fixed order.
 // The codes become bf16, times their scale, eight at a time on the way into the
 // 16x16x32 bf16 instruction (both e2m1 and e4m3 are exact in bf16).  The scaled
 // 8- and 4-bit instructions take them undecoded, but add the products of a step
 // at less than fp32's precision: 2^-16 of the sum of magnitudes was seen at
 // K = 128, and fp32 outputs are to keep their 24 bits.
+//
+// The address unit takes four lanes a clock if they share 64 bytes and one if they
+// do not, and the instruction wants its 16 rows from 16 neighbouring lanes: loads
+// straight into its operands run at a quarter of the rate.  That is enough for
+// the weights, of which each byte is loaded once (16 bytes a clock and CU: 9.8
+// TB/s), and not for the tokens, which every workgroup loads: they and the scales
+// are staged in LDS, in whole lines, and the waves of a workgroup split its rows.
+// Up to four tokens do not use the matrix instruction: 16 lanes take a row, the
+// tokens stay in registers, and the waves split K.
+// A vector instruction of one wave takes a SIMD 1.8 ns, so a few hundred of them
+// are as long as the memory's part of a small call: the loops below hold little
+// beside the conversions.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "row_ops.hpp"
 
@@ -19,207 +28,306 @@ namespace twell {
 
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int CHUNK = 128;       // K of one step: four blocks, one per 16 lanes
+constexpr int CHUNK = 128;       // K of one step of the matrix path: four blocks, one per 16 lanes
+constexpr int GROUP = 512;       // K a wave of the path without it takes at a time
 
-// Lane l's part of 16 rows (row l % 16) and one chunk (block l / 16) of W.
-struct WFrag {
-  uint4 q;
-  uint32_t s;
-};
-// The same part of 16 tokens (token l % 16), as loaded.
-template <bool MX>
-struct XFrag;
-template <>
-struct XFrag<true> {
-  uint4 q[2];
-  uint32_t s;
-};
-template <>
-struct XFrag<false> {
-  uint4 q[4];
-};
-
-struct WPtr {
-  const uint8_t* q;
-  const uint8_t* s;
-};
-struct XPtr {
-  const char* q;
-  const uint8_t* s;
-};
-
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 v;
+__device__ __forceinline__ u32x4 load16(const void* p) {
+  u32x4 v;
   memcpy(&v, p, 16);
   return v;
 }
 
-__device__ __forceinline__ WPtr w_ptr(const W4View& W, int K, int64_t n) {
-  const int b = (threadIdx.x >> 4) & 3;
-  return {W.code + n * (K / 2) + b * 16, W.scale + n * (K / 32) + b};
+// Between accesses of a wave's own LDS by different lanes.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <bool MX>
-__device__ __forceinline__ XPtr x_ptr(const W4Args& a, int64_t t) {
-  const int b = (threadIdx.x >> 4) & 3;
-  if constexpr (MX) return {(const char*)a.x + t * a.ldx + b * 32, a.x_scale + t * (a.K / 32) + b};
-  else return {(const char*)a.x + (t * a.ldx + b * 32) * 2, nullptr};
-}
+// A scale byte as fp32 2^(byte - 127); the conversions take the exponent bits as
+// they are (0 is 2^-127, 255 NaN).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-__device__ __forceinline__ WFrag load_w(const WPtr& p, int ck) {
-  return {*(const uint4*)(p.q + (int64_t)ck * 64), p.s[ck * 4]};
-}
-template <bool MX>
-__device__ __forceinline__ XFrag<MX> load_x(const XPtr& p, int ck) {
-  XFrag<MX> f;
-  if constexpr (MX) {
-    f.q[0] = load16(p.q + (int64_t)ck * 128);
-    f.q[1] = load16(p.q + (int64_t)ck * 128 + 16);
-    f.s = p.s[ck * 4];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.q[j] = load16(p.q + (int64_t)ck * 256 + j * 16);
-  }
-  return f;
-}
+__device__ __forceinline__ uint32_t dword(u32x4 q, int j) { return q[j]; }
 
-// The last chunk where K is no multiple of 128: blocks at and past `left` of it
-// count as zeros (of both operands: an infinity or NaN elsewhere must not meet
-// them) and are read from the chunk's first block.
-__device__ __forceinline__ WFrag load_w_tail(const WPtr& p, int ck, int left) {
-  const int b = (threadIdx.x >> 4) & 3, back = b < left ? 0 : b;
-  WFrag f{*(const uint4*)(p.q + (int64_t)ck * 64 - back * 16), p.s[ck * 4 - back]};
-  if (back) f = {make_uint4(0, 0, 0, 0), 127};
-  return f;
-}
-template <bool MX>
-__device__ __forceinline__ XFrag<MX> load_x_tail(const XPtr& p, int ck, int left) {
-  const int b = (threadIdx.x >> 4) & 3, back = b < left ? 0 : b;
-  constexpr int BLOCK = MX ? 32 : 64;
-  XFrag<MX> f;
-#pragma unroll
-  for (int j = 0; j < BLOCK / 16; ++j) {
-    f.q[j] = load16(p.q + (int64_t)ck * (4 * BLOCK) + j * 16 - back * BLOCK);
-    if (back) f.q[j] = make_uint4(0, 0, 0, 0);
-  }
-  if constexpr (MX) f.s = back ? 127 : p.s[ck * 4];
-  return f;
-}
+__device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 
-// Eight codes as bf16, times 2^(s - 127).
-__device__ __forceinline__ bf16x8 w_bf16(uint32_t codes, uint32_t s) {
-  const float scale = __uint_as_float(s << 23);      // the conversion takes the exponent bits: 0 is 2^-127, 255 NaN
+// Eight codes of weights as bf16, times scale.
+__device__ __forceinline__ bf16x8 w_bf16(uint32_t codes, float scale) {
   const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
   const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
   const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
   const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
   return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
-
-// Eight tokens' values as bf16, j of the block's four.
-template <bool MX>
-__device__ __forceinline__ bf16x8 x_bf16(const XFrag<MX>& x, int j) {
-  if constexpr (MX) {
-    const float scale = __uint_as_float(x.s << 23);
-    const uint4 q = x.q[j / 2];
-    const uint32_t lo = j & 1 ? q.z : q.x, hi = j & 1 ? q.w : q.y;
-    const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-    const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-    const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-    const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-    return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
-  } else {
-    return __builtin_bit_cast(bf16x8, x.q[j]);
-  }
+// acc[I ..] += v times eight codes of weights, times scale.
+template <int I>
+__device__ __forceinline__ void add8(uint32_t codes, float scale, float v, float acc[32]) {
+  const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 0);
+  const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 1);
+  const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 2);
+  const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 3);
+  const float w[8] = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[I + i] += v * w[i];
+}
+// Eight codes of tokens as bf16, times scale.
+__device__ __forceinline__ u32x4 x_bf16(uint32_t lo, uint32_t hi, float scale) {
+  return u32x4{bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
+                    bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
+                    bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false)),
+                    bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
 }
 
-// acc[r][t] += rows of w[r] x tokens of x[t] over one chunk; lane l's register
-// i is row 4 (l / 16) + i of token l % 16.
-template <bool MX, int RT, int TT>
-__device__ __forceinline__ void chunk_mma(const WFrag w[RT], const XFrag<MX> x[TT], f32x4 acc[RT][TT]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bf16x8 B[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) B[t] = x_bf16<MX>(x[t], j);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const bf16x8 A = w_bf16(j == 0 ? w[r].q.x : j == 1 ? w[r].q.y : j == 2 ? w[r].q.z : w[r].q.w, w[r].s);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[t], acc[r][t], 0, 0, 0);
-    }
-  }
-}
+// ---------------------------------------------------------------- the matrix path
 
-// Row tiles, token tiles of a workgroup; its waves, which split K; chunks a wave
-// has in flight.
-template <bool MX_, int RT_, int TT_, int NW_, int U_>
+// The waves of a workgroup split K; each has RT tiles of 16 rows times TT tiles of
+// 16 tokens, and the registers of OCC workgroups a CU.
+template <bool MX_, int RT_, int TT_, int OCC_>
 struct Tile {
   static constexpr bool MX = MX_;
-  static constexpr int RT = RT_, TT = TT_, NW = NW_, U = U_, NTH = 64 * NW, E = RT * TT;   // E: 16x16 results
-  static constexpr int EPW = (E + NW - 1) / NW;      // of them per wave after the sum
+  static constexpr int RT = RT_, TT = TT_, ROWS = 16 * RT, TOKS = 16 * TT;
+  static constexpr int E = RT * TT;                  // 16x16 results
+  static constexpr int OCC = OCC_;
+  static constexpr int XB = MX ? 128 : 256;          // bytes of a token's chunk
+  static constexpr int XP = XB + 16;                 // and of its row in LDS: 16 tokens' same unit lies in all banks
+  static constexpr int XL = XB * 16 / 1024;          // loads of a chunk of 16 tokens
 };
-
-// Sums of the workgroup's rows (n[r]: this lane's row of tile r) and tokens over
-// K: wave w returns results e = w, w + NW, ... of index r * TT + t.
+constexpr int WP = 80;                               // the same of 64 bytes of a row's codes
+// A wave's piece of LDS.
 template <class C>
-__device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, const int64_t n[C::RT], int t0,
-                                             f32x4 (*red)[C::E][64], f32x4 out[C::EPW]) {
-  constexpr int RT = C::RT, TT = C::TT, NW = C::NW, U = C::U;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  WPtr wp[RT];
-  XPtr xp[TT];
+struct WaveLds {
+  char x[C::TOKS * C::XP];
+  char w[C::ROWS * WP];
+  uint32_t s[C::RT][16 * 4];                         // a group's scales, a chunk's four a dword
+  uint32_t xs[C::MX ? C::TT : 1][16 * 4];
+};
+// A workgroup's, for its waves: their pieces, and then their sums over them.
+template <class C>
+int tile_lds(int waves) {
+  const size_t a = sizeof(WaveLds<C>), b = sizeof(f32x4) * 64 * C::E;
+  return waves * (int)(a > b ? a : b);
+}
+
+// Byte hi of a dword of scales at the exponent's place of an fp32 (the conversions
+// take no other bits of it).
+__device__ __forceinline__ float scale_at(uint32_t s, int hi) {
+  return __uint_as_float(__builtin_rotateright32(s, 9 + 8 * hi));
+}
+
+// Four scales of a row from block b on, a byte each (blocks past the row's end: its
+// last one, not used).
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int b, int blocks) {
+  uint32_t v;
+  if (blocks % 4 == 0) {
+    memcpy(&v, p + min(b, blocks - 4), 4);
+  } else {
+    const uint32_t v0 = p[min(b, blocks - 1)], v1 = p[min(b + 1, blocks - 1)];
+    const uint32_t v2 = p[min(b + 2, blocks - 1)], v3 = p[min(b + 3, blocks - 1)];
+    v = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+  }
+  return v;
+}
+
+// Sums over K of 16 RT rows (row(i): the row of W behind row i) and the tokens from
+// t0: wave w of `waves` gets results e = w, w + waves, ... of index r * TT + t in
+// out(e, sum); lane l's register i is row 4 (l / 16) + i of token l % 16.
+// Whole groups of K go round the waves, and then the chunks past them.
+template <class C, class Row, class Out>
+__device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, Row row, int t0, char* lds, Out out) {
+  constexpr int RT = C::RT, TT = C::TT, XL = C::XL;
+  constexpr bool MX = C::MX;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int lo = lane & 15, hi = lane >> 4;
+  const int blocks = a.K / 32, groups = a.K / GROUP, chunks = (blocks + 3) / 4;
+  WaveLds<C>& my = *(WaveLds<C>*)(lds + w * sizeof(WaveLds<C>));
+  // This lane's addresses: a block of a chunk and a chunk's scales of row lane / 4,
+  // and 16 bytes of a token of each load.
+  const uint8_t *wp[RT], *sp[RT], *xsp[TT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) wp[r] = w_ptr(W, a.K, n[r]);
+  for (int r = 0; r < RT; ++r) {
+    const int64_t n = row(16 * r + lane / 4);
+    wp[r] = W.code + n * (a.K / 2);
+    sp[r] = W.scale + n * blocks;
+  }
+  constexpr int TPL = 16 / XL;                       // tokens of a load
+  const char* xp[TT][XL];
+  const int xt = lane / (64 / TPL), xu = lane % (64 / TPL) * 16;
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xp[t] = x_ptr<C::MX>(a, min(t0 + 16 * t + (lane & 15), a.T - 1));
+  for (int t = 0; t < TT; ++t) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      xp[t][i] = (const char*)a.x + (int64_t)min(t0 + 16 * t + i * TPL + xt, a.T - 1) * a.ldx * (MX ? 1 : 2);
+    xsp[t] = MX ? a.x_scale + (int64_t)min(t0 + 16 * t + lane / 4, a.T - 1) * blocks : nullptr;
+  }
+  char* const xw = my.x + xt * C::XP + xu;
+  char* const ww = my.w + (lane / 4) * WP + (lane & 3) * 16;
+  const char* const xr = my.x + lo * C::XP + hi * (C::XB / 4);   // block hi of token lo
+  const char* const wr = my.w + lo * WP + hi * 16;               // block hi of row lo
+
   f32x4 acc[RT][TT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int full = a.K / CHUNK, left = (a.K % CHUNK) / 32;
-  for (int ck = w; ck < full; ck += NW * U) {
-    // All loads of U chunks first; one past the end repeats the last (no branch
-    // between loads) and is not used.
-    WFrag wf[U][RT];
-    XFrag<C::MX> xf[U][TT];
+  // One chunk from LDS, with its blocks' scales, a byte each; blocks from `nb` on
+  // count as zeros of both operands (an infinity or a NaN of one must not meet what
+  // was read for the other).
+  auto multiply = [&](const uint32_t (&sc)[RT], const uint32_t (&xsc)[TT], int nb) {
+    u32x4 q[RT], x[TT][XL];
+    float ws[RT], xs[TT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = min(ck + u * NW, full - 1);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) wf[u][r] = load_w(wp[r], c);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) xf[u][t] = load_x<C::MX>(xp[t], c);
+    for (int r = 0; r < RT; ++r) {
+      q[r] = *(const u32x4*)(wr + 16 * r * WP);
+      ws[r] = scale_at(sc[r], hi);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (ck + u * NW < full) chunk_mma<C::MX, RT, TT>(wf[u], xf[u], acc);
-  }
-  if (left && w == full % NW) {
-    WFrag wf[RT];
-    XFrag<C::MX> xf[TT];
+    for (int t = 0; t < TT; ++t) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) wf[r] = load_w_tail(wp[r], full, left);
+      for (int j = 0; j < XL; ++j) x[t][j] = *(const u32x4*)(xr + 16 * t * C::XP + j * 16);
+      xs[t] = MX ? scale_at(xsc[t], hi) : 1.f;
+    }
+    if (nb < 4) {
+      const bool in = hi < nb;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) xf[t] = load_x_tail<C::MX>(xp[t], full, left);
-    chunk_mma<C::MX, RT, TT>(wf, xf, acc);
+      for (int r = 0; r < RT; ++r) {
+        q[r] = in ? q[r] : u32x4{0, 0, 0, 0};
+        ws[r] = in ? ws[r] : 1.f;
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        xs[t] = in ? xs[t] : 1.f;
+#pragma unroll
+        for (int j = 0; j < XL; ++j) x[t][j] = in ? x[t][j] : u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf16x8 B[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if constexpr (MX) {
+          B[t] = __builtin_bit_cast(bf16x8, x_bf16(dword(x[t][j / 2], 2 * (j & 1)), dword(x[t][j / 2], 2 * (j & 1) + 1), xs[t]));
+        } else {
+          B[t] = __builtin_bit_cast(bf16x8, x[t][j]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const bf16x8 A = w_bf16(dword(q[r], j), ws[r]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[t], acc[r][t], 0, 0, 0);
+      }
+    }
+  };
+
+  if (w < groups) {
+    u32x4 wf[RT], xf[TT][XL];                        // one chunk in flight: more cost waves
+    uint32_t sf[RT], xsf[TT] = {};
+    const int wo = (lane & 3) * 16;
+    auto load = [&](int ck) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) wf[r] = *(const u32x4*)(wp[r] + ck * 64 + wo);
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < XL; ++i) xf[t][i] = load16(xp[t][i] + ck * C::XB + xu);
+    };
+    auto load_group_scales = [&](int g) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sf[r] = load_scales(sp[r], g * 16 + (lane & 3) * 4, blocks);
+      if constexpr (MX) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) xsf[t] = load_scales(xsp[t], g * 16 + (lane & 3) * 4, blocks);
+      }
+    };
+    load_group_scales(w);
+    load(4 * w);
+#pragma unroll 1
+    for (int g = w; g < groups; g += waves) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) my.s[r][lane] = sf[r];
+      if constexpr (MX) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) my.xs[t][lane] = xsf[t];
+      }
+      u32x4 sc[RT], xsc[TT];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) *(u32x4*)(ww + 16 * r * WP) = wf[r];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = xf[t][i];
+        wave_lds_fence();
+        if (c == 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) sc[r] = *(const u32x4*)&my.s[r][4 * lo];
+          if constexpr (MX) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) xsc[t] = *(const u32x4*)&my.xs[t][4 * lo];
+          }
+        }
+        if (c < 3) {
+          load(4 * g + c + 1);
+        } else if (g + waves < groups) {
+          load_group_scales(g + waves);
+          load(4 * (g + waves));
+        }
+        uint32_t s[RT], xs[TT] = {};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = sc[r][c];
+        if constexpr (MX) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) xs[t] = xsc[t][c];
+        }
+        multiply(s, xs, 4);
+        wave_lds_fence();
+      }
+    }
   }
+#pragma unroll 1
+  for (int ck = groups * 4 + w; ck < chunks; ck += waves) {
+    uint32_t s[RT], xs[TT] = {};
+    const int wo = min(ck * 4 + (lane & 3), blocks - 1) * 16, xo = min(ck * C::XB + xu, blocks * (C::XB / 4) - 16);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      *(u32x4*)(ww + 16 * r * WP) = *(const u32x4*)(wp[r] + wo);
+      my.s[r][lane] = load_scales(sp[r], ck * 4, blocks);
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = load16(xp[t][i] + xo);
+      if constexpr (MX) my.xs[t][lane] = load_scales(xsp[t], ck * 4, blocks);
+    }
+    wave_lds_fence();
+    // load_scales starts at the last four blocks where they are whole chunks, so at ck's
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s[r] = my.s[r][4 * lo];
+    if constexpr (MX) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xs[t] = my.xs[t][4 * lo];
+    }
+    multiply(s, xs, blocks - 4 * ck);
+    wave_lds_fence();
+  }
+  __syncthreads();                                   // the sums lie over the waves' pieces
+  f32x4 (*sum)[C::E][64] = (f32x4(*)[C::E][64])lds;
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) red[w][r * TT + t][lane] = acc[r][t];
+    for (int t = 0; t < TT; ++t) sum[w][r * TT + t][lane] = acc[r][t];
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < C::EPW; ++k) {
-    const int e = w + k * NW;
-    if (e < C::E) {
-      out[k] = red[0][e][lane];
-#pragma unroll
-      for (int i = 1; i < NW; ++i) out[k] += red[i][e][lane];
-    }
+  for (int e = w; e < C::E; e += waves) {
+    f32x4 v = sum[0][e][lane];
+    for (int i = 1; i < waves; ++i) v += sum[i][e][lane];
+    out(e, v);
   }
 }
 
@@ -231,26 +339,20 @@ __device__ __forceinline__ f32x4 bias4(const W4Args& a, int64_t n) {
   return b;
 }
 
+constexpr int TILE_WAVES = 4;
+extern __shared__ __attribute__((aligned(16))) char dyn_lds[];
+
 }  // namespace
 
 template <class C>
-__global__ __launch_bounds__(C::NTH) void w4_matvec_kernel(W4Args a) {
-  __shared__ f32x4 red[C::NW][C::E][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * C::RT);
-  for (int t0 = blockIdx.y * (16 * C::TT); t0 < a.T; t0 += gridDim.y * (16 * C::TT)) {
-    int64_t n[C::RT];
-#pragma unroll
-    for (int r = 0; r < C::RT; ++r) n[r] = min(n0 + 16 * r + (lane & 15), (int64_t)a.N - 1);
-    f32x4 v[C::EPW];
-    tile_product<C>(a, a.W, n, t0, red, v);
-#pragma unroll
-    for (int k = 0; k < C::EPW; ++k) {
-      const int e = w + k * C::NW;
-      if (e >= C::E) break;
+__global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_matvec_kernel(W4Args a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t n0 = (int64_t)blockIdx.x * C::ROWS;
+  for (int t0 = blockIdx.y * C::TOKS; t0 < a.T; t0 += gridDim.y * C::TOKS) {
+    tile_product<C>(a, a.W, [&](int i) { return min(n0 + i, (int64_t)a.N - 1); }, t0, dyn_lds, [&](int e, f32x4 o) {
       const int64_t t = t0 + 16 * (e % C::TT) + (lane & 15), m = n0 + 16 * (e / C::TT) + 4 * (lane >> 4);
-      if (t >= a.T || m >= a.N) continue;
-      const f32x4 o = v[k] + bias4(a, m);
+      if (t >= a.T || m >= a.N) return;
+      o += bias4(a, m);
       const int left = (int)min((int64_t)4, a.N - m);
       if (a.y_bf16) {
         uint16_t* y = (uint16_t*)a.y + t * a.ldy + m;
@@ -272,82 +374,253 @@ __global__ __launch_bounds__(C::NTH) void w4_matvec_kernel(W4Args a) {
             if (i < left) y[i] = o[i];
         }
       }
-    }
+    });
     __syncthreads();
   }
 }
 
-// The layer's gate and up products of 16 RT neurons: g = x . Wg^T + bg; where a
-// neuron fires (g > 0) for some token of the workgroup, u = x . Wu^T on the
-// neurons that fire, and a = g u is stored for the pairs that do, with a bit for
-// each pair.  Rows of Wu that no token fires are not read: their lanes take the
-// addresses of one that is.
+// The layer's gate and up products of a workgroup's neurons: g = x . Wg^T + bg;
+// where a neuron fires (g > 0) for some token of the workgroup, u = x . Wu^T on the
+// neurons that fire, listed, and a = g u is stored for the pairs that do, with a bit
+// for each pair.  Other rows of Wu are not read.  F is a multiple of the
+// workgroup's rows.
 template <class C>
-__global__ __launch_bounds__(C::NTH) void w4_gate_up_kernel(W4Args a) {
-  __shared__ f32x4 red[C::NW][C::E][64];
-  __shared__ uint32_t fires[C::RT];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * (16 * C::RT);
-  for (int t0 = blockIdx.y * (16 * C::TT); t0 < a.T; t0 += gridDim.y * (16 * C::TT)) {
-    int64_t n[C::RT];
-#pragma unroll
-    for (int r = 0; r < C::RT; ++r) n[r] = n0 + 16 * r + (lane & 15);
+__global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_gate_up_kernel(W4Args a) {
+  using U = Tile<C::MX, 1, C::TT, C::OCC>;
+  __shared__ uint32_t fires[C::RT];                  // of each tile of 16 rows
+  __shared__ float hl[C::TOKS][C::ROWS + 1];         // max(g, 0), NaN as 0
+  __shared__ int list[C::ROWS];                      // the rows that fire
+  const int lane = threadIdx.x & 63, n0 = blockIdx.x * C::ROWS;
+  for (int t0 = blockIdx.y * C::TOKS; t0 < a.T; t0 += gridDim.y * C::TOKS) {
     if (threadIdx.x < C::RT) fires[threadIdx.x] = 0;
-    f32x4 h[C::EPW], u[C::EPW];
-    tile_product<C>(a, a.W, n, t0, red, h);            // has a barrier after the line above
-#pragma unroll
-    for (int k = 0; k < C::EPW; ++k) {
-      const int e = w + k * C::NW;
-      if (e >= C::E) break;
-      const int t = t0 + 16 * (e % C::TT) + (lane & 15), q = lane >> 4;
-      h[k] += bias4(a, n0 + 16 * (e / C::TT) + 4 * q);
+    tile_product<C>(a, a.W, [&](int i) { return (int64_t)(n0 + i); }, t0, dyn_lds, [&](int e, f32x4 h) {
+      const int tl = 16 * (e % C::TT) + (lane & 15), t = t0 + tl, q = lane >> 4, r0 = 16 * (e / C::TT);
+      h += bias4(a, n0 + r0 + 4 * q);
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m |= (t < a.T && h[k][i] > 0.f) ? 1u << (4 * q + i) : 0u;
+      for (int i = 0; i < 4; ++i) {
+        const bool f = t < a.T && h[i] > 0.f;
+        m |= f ? 1u << (4 * q + i) : 0u;
+        hl[tl][r0 + 4 * q + i] = f ? h[i] : 0.f;
+      }
       m |= __shfl_xor((int)m, 16);
       m |= __shfl_xor((int)m, 32);
-      if (q == 0 && t < a.T) a.mask[(int64_t)t * (a.N / 16) + n0 / 16 + e / C::TT] = (uint16_t)m;
+      if (q == 0 && t < a.T) a.mask[(int64_t)t * (a.N / 16) + (n0 + r0) / 16] = (uint16_t)m;
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) m |= __shfl_xor((int)m, o);
       if (lane == 0 && m) atomicOr(&fires[e / C::TT], m);
+    });
+    __syncthreads();
+    int count = 0;
+#pragma unroll
+    for (int r = 0; r < C::RT; ++r) {
+      const uint32_t m = fires[r];
+      if (threadIdx.x < 16 && ((m >> lane) & 1)) list[count + __builtin_popcount(m & ((1u << lane) - 1))] = 16 * r + lane;
+      count += __builtin_popcount(m);
     }
     __syncthreads();
-    int first = -1;
+    auto up = [&](auto tile) {
+      using V = decltype(tile);
+      tile_product<V>(
+          a, a.Wu, [&](int i) { return (int64_t)(n0 + list[min(i, count - 1)]); }, t0, dyn_lds, [&](int e, f32x4 u) {
+            const int tl = 16 * (e % V::TT) + (lane & 15);
 #pragma unroll
-    for (int r = C::RT - 1; r >= 0; --r)
-      if (fires[r]) first = n0 + 16 * r + __builtin_ctz(fires[r]);
-    if (first >= 0) {
-#pragma unroll
-      for (int r = 0; r < C::RT; ++r) n[r] = (fires[r] >> (lane & 15)) & 1 ? n[r] : first;
-      tile_product<C>(a, a.Wu, n, t0, red, u);
-#pragma unroll
-      for (int k = 0; k < C::EPW; ++k) {
-        const int e = w + k * C::NW;
-        if (e >= C::E) break;
-        const int64_t t = t0 + 16 * (e % C::TT) + (lane & 15);
-        f32x4 v;
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = h[k][i] > 0.f ? h[k][i] * u[k][i] : 0.f;
-          any |= h[k][i] > 0.f;
-        }
-        if (any && t < a.T) *(f32x4*)(a.act + t * a.N + n0 + 16 * (e / C::TT) + 4 * (lane >> 4)) = v;
-      }
-    }
+            for (int i = 0; i < 4; ++i) {
+              const int k = 16 * (e / V::TT) + 4 * (lane >> 4) + i;
+              if (k < count) {
+                const float h = hl[tl][list[k]];
+                if (h > 0.f) a.act[(int64_t)(t0 + tl) * a.N + n0 + list[k]] = h * u[i];
+              }
+            }
+          });
+    };
+    if (count > 16) up(C{});
+    else if (count > 0) up(U{});
     __syncthreads();
   }
 }
+
+// ---------------------------------------------------------------- up to four tokens
+
+namespace {
+
+constexpr int GEMV_ROWS = 16, GEMV_WAVES = 8, GEMV_T = 2;
+
+// Sum over the 16 lanes of a row, in lane 15 of them.
+__device__ __forceinline__ float sum16(float v) {
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x111, 0xf, 0xf, true));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x112, 0xf, 0xf, true));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x114, 0xf, 0xf, true));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x118, 0xf, 0xf, true));
+  return v;
+}
+
+// A lane's block of weights of four rows, and its eight values of each token.
+template <int T>
+struct GemvLoads {
+  u32x4 q[GEMV_ROWS / 4];
+  uint32_t s[GEMV_ROWS / 4];
+  u32x4 x[T];
+  uint32_t xs[T];
+};
+template <int T, class Row>
+__device__ __forceinline__ void gemv_load(const W4Args& a, const W4View& W, Row row, int rows, int group,
+                                          GemvLoads<T>& f) {
+  const int lane = threadIdx.x & 63, blocks = a.K / 32, b = min(group * 16 + (lane & 15), blocks - 1);
+#pragma unroll
+  for (int i = 0; i < GEMV_ROWS / 4; ++i)
+    if (4 * i < rows) {
+      const int64_t n = row(min(4 * i + (lane >> 4), rows - 1)) * blocks + b;
+      f.q[i] = *(const u32x4*)(W.code + n * 16);
+      f.s[i] = W.scale[n];
+    }
+  const int u = min(group * 64 + lane, 4 * blocks - 1);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t tok = min(t, a.T - 1);
+    if (a.x_scale) {
+      u32x2 q;
+      memcpy(&q, (const char*)a.x + tok * a.ldx + 8 * u, 8);
+      f.x[t].x = q.x;
+      f.x[t].y = q.y;
+      f.xs[t] = a.x_scale[tok * blocks + u / 4];
+    } else {
+      f.x[t] = load16((const char*)a.x + (tok * a.ldx + 8 * u) * 2);
+    }
+  }
+}
+
+// part[wave][t][i]: the wave's part of row(i) . x_t for i < rows; f holds its first
+// group's loads.  16 lanes take a row, a block each, so that a load takes 256 bytes
+// of each of four rows; the tokens are loaded in whole lines and go through LDS
+// (the wave's own, no barrier) into the order of the blocks.
+template <int T, class Row>
+__device__ __forceinline__ void gemv(const W4Args& a, const W4View& W, Row row, int rows, GemvLoads<T>& f,
+                                     u32x4 (*xl)[T][64], float (*part)[T][GEMV_ROWS]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int blocks = a.K / 32;
+  float acc[GEMV_ROWS / 4][T] = {};
+  for (int g = wave;;) {
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      xl[wave][t][lane ^ ((lane >> 4) & 3)] = a.x_scale ? x_bf16(f.x[t].x, f.x[t].y, scale_of(f.xs[t])) : f.x[t];
+    wave_lds_fence();
+    u32x4 x[T][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = 4 * (lane & 15) + j;
+        x[t][j] = xl[wave][t][u ^ ((u >> 4) & 3)];
+      }
+    wave_lds_fence();
+    if (g * 16 + (lane & 15) < blocks) {
+#pragma unroll
+      for (int i = 0; i < GEMV_ROWS / 4; ++i)
+        if (4 * i < rows) {
+          const float s = scale_of(f.s[i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8 w = w_bf16(dword(f.q[i], j), s);
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              const bf16x8 v = __builtin_bit_cast(bf16x8, x[t][j]);
+#pragma unroll
+              for (int k = 0; k < 8; k += 2)
+                acc[i][t] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[k], w[k + 1]}, bf16x2{v[k], v[k + 1]}, acc[i][t], false);
+            }
+          }
+        }
+    }
+    g += waves;
+    if (g * 16 >= blocks) break;
+    gemv_load<T>(a, W, row, rows, g, f);
+  }
+#pragma unroll
+  for (int i = 0; i < GEMV_ROWS / 4; ++i)
+    if (4 * i < rows) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const float v = sum16(acc[i][t]);
+        if ((lane & 15) == 15) part[wave][t][4 * i + (lane >> 4)] = v;
+      }
+    }
+}
+
+}  // namespace
+
+template <int T>
+__global__ __launch_bounds__(64 * GEMV_WAVES) void w4_gemv_kernel(W4Args a) {
+  __shared__ u32x4 xl[GEMV_WAVES][T][64];
+  __shared__ float part[GEMV_WAVES][T][GEMV_ROWS];
+  const int64_t n0 = (int64_t)blockIdx.x * GEMV_ROWS;
+  const int rows = (int)min((int64_t)GEMV_ROWS, a.N - n0);
+  auto row = [&](int i) { return n0 + i; };
+  GemvLoads<T> f;
+  gemv_load<T>(a, a.W, row, rows, threadIdx.x >> 6, f);
+  gemv<T>(a, a.W, row, rows, f, xl, part);
+  __syncthreads();
+  const int i = threadIdx.x % GEMV_ROWS, t = threadIdx.x / GEMV_ROWS;
+  if (t >= min(T, a.T) || i >= rows) return;
+  float v = part[0][t][i];
+  for (int w = 1; w < (int)(blockDim.x >> 6); ++w) v += part[w][t][i];
+  if (a.bias) v += bf16_to_f32(a.bias[n0 + i]);
+  if (a.y_bf16) ((uint16_t*)a.y)[t * a.ldy + n0 + i] = (uint16_t)bf16_round(v);
+  else ((float*)a.y)[t * a.ldy + n0 + i] = v;
+}
+
+// The layer's gate and up products of 16 neurons, as w4_gate_up_kernel.
+template <int T>
+__global__ __launch_bounds__(64 * GEMV_WAVES) void w4_gate_up_gemv_kernel(W4Args a) {
+  __shared__ u32x4 xl[GEMV_WAVES][T][64];
+  __shared__ float part[GEMV_WAVES][T][GEMV_ROWS];
+  const int64_t n0 = (int64_t)blockIdx.x * GEMV_ROWS;
+  auto row = [&](int i) { return n0 + i; };
+  GemvLoads<T> f;
+  gemv_load<T>(a, a.W, row, GEMV_ROWS, threadIdx.x >> 6, f);
+  gemv<T>(a, a.W, row, GEMV_ROWS, f, xl, part);
+  __syncthreads();
+  // every wave adds and packs for itself: lane 16 t + i has token t, row i
+  const int lane = threadIdx.x & 63, i = lane & 15, t = lane >> 4, waves = blockDim.x >> 6;
+  const bool live = t < T && t < a.T;
+  float h = 0.f;
+  if (live) {
+    for (int w = 0; w < waves; ++w) h += part[w][t][i];
+    if (a.bias) h += bf16_to_f32(a.bias[n0 + i]);
+  }
+  const uint64_t m = ballot(live && h > 0.f);
+  const uint32_t any = (uint32_t)(m | m >> 16 | m >> 32 | m >> 48) & 0xffffu;      // neurons that fire for some token
+  if (threadIdx.x < 64 && i == 0 && live) a.mask[(int64_t)t * (a.N / 16) + blockIdx.x] = (uint16_t)(m >> (16 * t));
+  if (!any) return;
+  const int rows = __builtin_popcount(any);
+  auto fired = [&](int k) {                            // the k-th of them
+    uint32_t r = any;
+    for (; k > 0; --k) r &= r - 1;
+    return n0 + __builtin_ctz(r);
+  };
+  gemv_load<T>(a, a.Wu, fired, rows, threadIdx.x >> 6, f);
+  __syncthreads();                                     // part is read
+  gemv<T>(a, a.Wu, fired, rows, f, xl, part);
+  __syncthreads();
+  if (threadIdx.x < 64 && h > 0.f) {
+    const int k = __builtin_popcount(any & ((1u << i) - 1));
+    float u = 0.f;
+    for (int w = 0; w < waves; ++w) u += part[w][t][k];
+    a.act[(int64_t)t * a.N + n0 + i] = h * u;
+  }
+}
+
+// ---------------------------------------------------------------- the down product
 
 // y_t = sum over the pairs (t, n) that fire, n ascending within a slot, of
 // a * Wd[n].  One workgroup per token and DB blocks of 32 columns: the pairs are
 // listed in LDS from their bits, NS slots take every NS-th pair, a thread one
 // slot and one block (16 bytes of codes, one scale), and the slots are added in
 // order.
-constexpr int DB = 8, NS = 32, DLIST = 2048;
+constexpr int DB = 8, NS = 32, DU = 4, DLIST = 2048;
+
 __global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
   __shared__ int ln[DLIST];
-  __shared__ float la[DLIST];
   __shared__ float part[NS][DB][33];
   __shared__ int wsum[DB * NS / 64];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -384,26 +657,25 @@ __global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
         }
         __syncthreads();
         const int cntr = min(DLIST, total - e0);
-        for (int i = tid; i < cntr; i += DB * NS) la[i] = act[ln[i]];
-        __syncthreads();
         if (live)
-          for (int i = slot; i < cntr; i += NS) {
-            const int64_t n = ln[i];
-            const float v = la[i];
-            const uint4 q = *(const uint4*)(a.Wd.code + n * (a.K / 2) + b * 16);
-            const float s = __uint_as_float((uint32_t)a.Wd.scale[n * nblk + b] << 23);
-            const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+          for (int i0 = slot; i0 < cntr; i0 += NS * DU) {
+            u32x4 q[DU];
+            float v[DU], sc[DU];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#define TWELL_PAIR(k)                                                          \
-    {                                                                            \
-      const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[j], s, k);       \
-      acc[8 * j + 2 * k] += v * p[0];                                            \
-      acc[8 * j + 2 * k + 1] += v * p[1];                                        \
-    }
-              TWELL_PAIR(0) TWELL_PAIR(1) TWELL_PAIR(2) TWELL_PAIR(3)
-#undef TWELL_PAIR
+            for (int u = 0; u < DU; ++u) {
+              const int64_t n = ln[min(i0 + u * NS, cntr - 1)];
+              v[u] = act[n];
+              q[u] = *(const u32x4*)(a.Wd.code + n * (a.K / 2) + b * 16);
+              sc[u] = __uint_as_float((uint32_t)a.Wd.scale[n * nblk + b] << 23);
             }
+#pragma unroll
+            for (int u = 0; u < DU; ++u)
+              if (i0 + u * NS < cntr) {
+                add8<0>(q[u].x, sc[u], v[u], acc);
+                add8<8>(q[u].y, sc[u], v[u], acc);
+                add8<16>(q[u].z, sc[u], v[u], acc);
+                add8<24>(q[u].w, sc[u], v[u], acc);
+              }
           }
         __syncthreads();
       }
@@ -425,35 +697,58 @@ __global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
 
 namespace {
 
-// Calls f with the tile for T tokens and N rows.
-template <bool MX, class F>
-void with_tile(int T, int64_t N, F f) {
-  if (T <= 16) {
-    if (N <= 16384) f(Tile<MX, 1, 1, 8, 2>{});
-    else f(Tile<MX, 2, 1, 4, 2>{});
-  } else if (T <= 32) {
-    f(Tile<MX, 1, 2, 4, 2>{});
-  } else {
-    f(Tile<MX, 1, 4, 4, 1>{});
-  }
+// Calls f with the tile for the tokens and rows: 32 rows x 16 tokens, the most
+// workgroups and waves, unless there are enough workgroups of 64 x 32, which read
+// the tokens half as often (64 tokens: 40001 x 2048, 29 us and 42 with the small
+// tile; 5632 x 2048, 8.0 and 7.4).
+template <class F>
+void with_tile(const W4Args& a, bool layer, F f) {
+  auto go = [&](auto mx) {
+    constexpr bool MX = decltype(mx)::value;
+    if (!layer && a.T > 16 && a.N > 16384) f(Tile<MX, 4, 2, 2>{});
+    else f(Tile<MX, 2, 1, 1>{});
+  };
+  if (a.x_scale) go(std::true_type{});
+  else go(std::false_type{});
 }
 
-template <class F>
-void with_tile(const W4Args& a, F f) {
-  if (a.x_scale) with_tile<true>(a.T, a.N, f);
-  else with_tile<false>(a.T, a.N, f);
+// Waves of a workgroup: one per group of K, up to `most`.
+int waves_of(const W4Args& a, int most) {
+  const int groups = (a.K + GROUP - 1) / GROUP;
+  return groups < most ? groups : most;
 }
 
 constexpr int TOKEN_GRID = 1024;      // workgroups along the tokens; more tokens are walked in a loop
 
+template <class C>
+dim3 tile_grid(const W4Args& a) {
+  const int toks = (a.T + C::TOKS - 1) / C::TOKS;
+  return dim3((a.N + C::ROWS - 1) / C::ROWS, toks < TOKEN_GRID ? toks : TOKEN_GRID);
+}
+
+bool use_gemv(const W4Args& a) { return a.T <= GEMV_T; }
+
+// Calls f with the tokens of the kernel and its workgroup.
+template <class F>
+void with_gemv(const W4Args& a, F f) {
+  const int threads = 64 * waves_of(a, GEMV_WAVES);
+  if (a.T == 1) f(std::integral_constant<int, 1>{}, threads);
+  else f(std::integral_constant<int, GEMV_T>{}, threads);
+}
+
 }  // namespace
 
 hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s) {
-  with_tile(a, [&](auto c) {
-    using C = decltype(c);
-    const int rows = 16 * C::RT, toks = (a.T + 16 * C::TT - 1) / (16 * C::TT);
-    w4_matvec_kernel<C><<<dim3((a.N + rows - 1) / rows, toks < TOKEN_GRID ? toks : TOKEN_GRID), C::NTH, 0, s>>>(a);
-  });
+  if (use_gemv(a)) {
+    with_gemv(a, [&](auto t, int threads) {
+      w4_gemv_kernel<t.value><<<dim3((a.N + GEMV_ROWS - 1) / GEMV_ROWS), threads, 0, s>>>(a);
+    });
+  } else {
+    with_tile(a, false, [&](auto c) {
+      using C = decltype(c);
+      w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
+    });
+  }
   return hipGetLastError();
 }
 
@@ -465,11 +760,16 @@ size_t ffn_w4_ws_bytes(int T, int d, int F) {
 hipError_t launch_ffn_w4(W4Args a, void* ws, hipStream_t s) {
   a.act = (float*)ws;
   a.mask = (uint16_t*)((char*)ws + (size_t)a.T * a.N * 4);
-  with_tile(a, [&](auto c) {
-    using C = decltype(c);
-    const int rows = 16 * C::RT, toks = (a.T + 16 * C::TT - 1) / (16 * C::TT);
-    w4_gate_up_kernel<C><<<dim3(a.N / rows, toks < TOKEN_GRID ? toks : TOKEN_GRID), C::NTH, 0, s>>>(a);
-  });
+  if (use_gemv(a)) {
+    with_gemv(a, [&](auto t, int threads) {
+      w4_gate_up_gemv_kernel<t.value><<<dim3(a.N / GEMV_ROWS), threads, 0, s>>>(a);
+    });
+  } else {
+    with_tile(a, true, [&](auto c) {
+      using C = decltype(c);
+      w4_gate_up_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
+    });
+  }
   w4_down_kernel<<<dim3((a.K + DB * 32 - 1) / (DB * 32), a.T < TOKEN_GRID ? a.T : TOKEN_GRID), DB * NS, 0, s>>>(a);
   return hipGetLastError();
 }
