@@ -1,6 +1,7 @@
 """ctypes binding of libtwell (include/twell.h).  Argument marshalling only:
 torch tensors become device pointers, the current torch stream becomes the
-hipStream_t, and a non-zero status raises TwellError.  Every step of the
+hipStream_t, and a non-zero status raises TwellError.  The calls around the layer
+and on 4-bit weights are marshalled by a native module (csrc/bind.cpp).  Every step of the
 computation runs in the library's HIP kernels; nothing here computes."""
 from __future__ import annotations
 
@@ -485,41 +486,36 @@ def norm_shape(T: int, d: int, x_dt: int, res_dt: int, y_dt: int, w_dt: int, eps
     return c_twell_norm_shape(T, d, x_dt, res_dt, y_dt, w_dt, eps, p)
 
 
-def _mat(t, T: int, d: int, size: int, name: str):
-    """(pointer, row stride) of a [T][d] matrix with contiguous rows of
-    `size`-byte elements."""
-    if t is None:
-        return None, 0
-    if t.shape != (T, d) or t.element_size() != size or (d > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected [{T}][{d}] of {size}-byte elements with contiguous rows, got "
-                         f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
-    return t.data_ptr(), t.stride(0)
+_bind_module = None
 
 
-def _vec(t, n: int, size: int, name: str):
-    if t is None:
-        return None
-    if t.numel() != n or t.element_size() != size or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous {size}-byte elements, got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
+def _bind():
+    """The native marshalling module (csrc/bind.cpp); like the library it has to
+    be built, and there is no fallback."""
+    global _bind_module
+    if _bind_module is None:
+        import importlib.machinery
+        import importlib.util
 
-
-_SIZE = {TWELL_F32: 4, TWELL_BF16: 2, TWELL_MXFP8: 1}
-
-
-def _size(dt: int) -> int:
-    return _SIZE.get(dt, 1)
+        import torch  # noqa: F401  its libraries are the module's
+        lib()
+        path = os.path.join(PKG, "lib", "_twell_bind.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m activation_sparse_feedforward_gate_amd.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_twell_bind", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_twell_bind", loader))
+        loader.exec_module(module)
+        _bind_module = module
+    return _bind_module
 
 
 def twell_add_rmsnorm_fwd(shape: c_twell_norm_shape, x, residual, w, rng, sum, y, y_scale=None, rstd=None,
                           stream=None) -> None:
     """sum = residual + dropout(x); y = its root-mean-square norm times w."""
-    T, d, res = shape.T, shape.d, _size(shape.res_dt)
-    _check(lib().twell_add_rmsnorm_fwd(
-        shape, *_mat(x, T, d, _size(shape.x_dt), "x"), *_mat(residual, T, d, res, "residual"),
-        _vec(w, d, _size(shape.w_dt), "w"), _vec(rng, 2, 8, "rng"), *_mat(sum, T, d, res, "sum"),
-        *_mat(y, T, d, _size(shape.y_dt), "y"), _vec(y_scale, T * -(-d // 32), 1, "y_scale"),
-        _vec(rstd, T, 4, "rstd"), _stream(stream)))
+    st = (_bind_module or _bind()).add_rmsnorm_fwd(shape, x, residual, w, rng, sum, y, y_scale, rstd, stream)
+    if st:
+        _check(st)
 
 
 def twell_add_rmsnorm_bwd_workspace(shape: c_twell_norm_shape) -> int:
@@ -529,20 +525,16 @@ def twell_add_rmsnorm_bwd_workspace(shape: c_twell_norm_shape) -> int:
 def twell_add_rmsnorm_bwd(shape: c_twell_norm_shape, dy, dsum, sum, w, rstd, rng, dres, dx, dw, ws,
                           stream=None) -> None:
     """The gradients of twell_add_rmsnorm_fwd from its stored sum and rstd."""
-    T, d, res = shape.T, shape.d, _size(shape.res_dt)
-    _check(lib().twell_add_rmsnorm_bwd(
-        shape, *_mat(dy, T, d, _size(shape.y_dt), "dy"), *_mat(dsum, T, d, res, "dsum"),
-        *_mat(sum, T, d, res, "sum"), _vec(w, d, _size(shape.w_dt), "w"), _vec(rstd, T, 4, "rstd"),
-        _vec(rng, 2, 8, "rng"), *_mat(dres, T, d, res, "dres"), *_mat(dx, T, d, _size(shape.x_dt), "dx"),
-        _vec(dw, d, 4, "dw"), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+    st = (_bind_module or _bind()).add_rmsnorm_bwd(shape, dy, dsum, sum, w, rstd, rng, dres, dx, dw, ws, stream)
+    if st:
+        _check(st)
 
 
 def twell_dropout_add(shape: c_twell_norm_shape, x, residual, rng, y, stream=None) -> None:
     """y = residual + dropout(x); with residual None also its own backward."""
-    T, d = shape.T, shape.d
-    _check(lib().twell_dropout_add(
-        shape, *_mat(x, T, d, _size(shape.x_dt), "x"), *_mat(residual, T, d, _size(shape.res_dt), "residual"),
-        _vec(rng, 2, 8, "rng"), *_mat(y, T, d, _size(shape.y_dt), "y"), _stream(stream)))
+    st = (_bind_module or _bind()).dropout_add(shape, x, residual, rng, y, stream)
+    if st:
+        _check(st)
 
 
 # ---------------------------------------------------------------- 4-bit weights
@@ -576,12 +568,9 @@ class TwellW4:
 
 def twell_w4_matvec(x, x_scale, W: TwellW4, bias, y, stream=None) -> None:
     """y = x . W^T + bias; x bf16, or MXFP8 with x_scale; y fp32 or bf16."""
-    T, N, K = x.shape[0], W.N, W.K
-    x_dt = TWELL_BF16 if x_scale is None else TWELL_MXFP8
-    px, ldx = _mat(x, T, K, _size(x_dt), "x")
-    py, ldy = _mat(y, T, N, _size(_dt(y.dtype)), "y")
-    _check(lib().twell_w4_matvec(T, px, x_dt, ldx, _vec(x_scale, T * (K // 32), 1, "x_scale"), W.c(),
-                                 _vec(bias, N, 2, "bias"), py, _dt(y.dtype), ldy, _stream(stream)))
+    st = (_bind_module or _bind()).w4_matvec(x, x_scale, W, bias, y, stream)
+    if st:
+        _check(st)
 
 
 def twell_ffn_fwd_w4_workspace(shape: c_twell_ffn_shape) -> int:
@@ -591,11 +580,9 @@ def twell_ffn_fwd_w4_workspace(shape: c_twell_ffn_shape) -> int:
 def twell_ffn_fwd_w4(shape: c_twell_ffn_shape, x, x_scale, Wg: TwellW4, bg, Wu: TwellW4, Wd: TwellW4, y, ws,
                      stream=None) -> None:
     """The layer on MXFP4 weights for few tokens; x bf16, or MXFP8 with x_scale."""
-    T, d, F = shape.T, shape.d, shape.F
-    _check(lib().twell_ffn_fwd_w4(
-        shape, _vec(x, T * d, _size(shape.in_dt), "x"), _vec(x_scale, T * (d // 32), 1, "x_scale"), Wg.c(),
-        _vec(bg, F, 2, "bg"), Wu.c(), Wd.c(), _vec(y, T * d, _size(shape.out_dt), "y"), _ptr(ws),
-        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+    st = (_bind_module or _bind()).ffn_fwd_w4(shape, x, x_scale, Wg, bg, Wu, Wd, y, ws, stream)
+    if st:
+        _check(st)
 
 
 def twell_status_string(st: int) -> str:

@@ -701,15 +701,17 @@ namespace {
 // workgroups and waves, unless there are enough workgroups of 64 x 32, which read
 // the tokens half as often (64 tokens: 40001 x 2048, 29 us and 42 with the small
 // tile; 5632 x 2048, 8.0 and 7.4).
+template <bool MX>
+using Small = Tile<MX, 2, 1, 3>;
+template <bool MX>
+using Large = Tile<MX, 4, 2, 2>;
 template <class F>
-void with_tile(const W4Args& a, bool layer, F f) {
-  auto go = [&](auto mx) {
-    constexpr bool MX = decltype(mx)::value;
-    if (!layer && a.T > 16 && a.N > 16384) f(Tile<MX, 4, 2, 2>{});
-    else f(Tile<MX, 2, 1, 1>{});
-  };
-  if (a.x_scale) go(std::true_type{});
-  else go(std::false_type{});
+void with_tile(const W4Args& a, F f) {
+  const bool large = a.T > 16 && a.N > 16384;
+  if (a.x_scale && large) f(Large<true>{});
+  else if (a.x_scale) f(Small<true>{});
+  else if (large) f(Large<false>{});
+  else f(Small<false>{});
 }
 
 // Waves of a workgroup: one per group of K, up to `most`.
@@ -744,7 +746,7 @@ hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s) {
       w4_gemv_kernel<t.value><<<dim3((a.N + GEMV_ROWS - 1) / GEMV_ROWS), threads, 0, s>>>(a);
     });
   } else {
-    with_tile(a, false, [&](auto c) {
+    with_tile(a, [&](auto c) {
       using C = decltype(c);
       w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
     });
@@ -765,10 +767,12 @@ hipError_t launch_ffn_w4(W4Args a, void* ws, hipStream_t s) {
       w4_gate_up_gemv_kernel<t.value><<<dim3(a.N / GEMV_ROWS), threads, 0, s>>>(a);
     });
   } else {
-    with_tile(a, true, [&](auto c) {
+    auto go = [&](auto c) {
       using C = decltype(c);
       w4_gate_up_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
-    });
+    };
+    if (a.x_scale) go(Small<true>{});
+    else go(Small<false>{});
   }
   w4_down_kernel<<<dim3((a.K + DB * 32 - 1) / (DB * 32), a.T < TOKEN_GRID ? a.T : TOKEN_GRID), DB * NS, 0, s>>>(a);
   return hipGetLastError();
