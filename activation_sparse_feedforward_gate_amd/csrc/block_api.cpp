@@ -72,6 +72,7 @@ twell_status w4(W4View* v, const twell_w4* W, const char* name) {
   if (!W) return FAIL(TWELL_EINVAL, "%s is NULL", name);
   if (W->N <= 0 || W->K <= 0) return FAIL(TWELL_EINVAL, "bad %s: N=%d K=%d", name, W->N, W->K);
   if (W->K % 32) return FAIL(TWELL_EUNSUPPORTED, "%s: K=%d is not a multiple of 32", name, W->K);
+  if (W->K >= 1 << 30) return FAIL(TWELL_EUNSUPPORTED, "%s: K=%d is not below 2^30", name, W->K);
   if (!W->codes || !W->scales) return FAIL(TWELL_EINVAL, "%s: NULL array", name);
   if ((uintptr_t)W->codes % 16) return FAIL(TWELL_EINVAL, "%s: codes are not 16-byte aligned", name);
   v->code = W->codes;

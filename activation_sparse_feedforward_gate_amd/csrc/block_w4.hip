@@ -10,15 +10,16 @@
 //
 // The address unit takes four lanes a clock if they share 64 bytes and one if they
 // do not, and the instruction wants its 16 rows from 16 neighbouring lanes: loads
-// straight into its operands run at a quarter of the rate.  That is enough for
-// the weights, of which each byte is loaded once (16 bytes a clock and CU: 9.8
-// TB/s), and not for the tokens, which every workgroup loads: they and the scales
-// are staged in LDS, in whole lines, and the waves of a workgroup split its rows.
-// Up to four tokens do not use the matrix instruction: 16 lanes take a row, the
+// straight into its operands run at a quarter of the rate.  Codes, tokens and scales
+// are loaded in whole lines instead and turned round in LDS, each wave in a piece of
+// its own with no barrier: the waves of a workgroup split K.
+// One and two tokens do not use the matrix instruction: 16 lanes take a row, the
 // tokens stay in registers, and the waves split K.
-// A vector instruction of one wave takes a SIMD 1.8 ns, so a few hundred of them
-// are as long as the memory's part of a small call: the loops below hold little
-// beside the conversions.
+// A vector instruction of a wave takes a SIMD 1.8 ns (the conversions are no slower
+// than others), so a few hundred of them are as long as the memory's part of a small
+// call: the loops below hold little beside the conversions.
+// 16 tokens, 40001 x 2048 (46 MB): 12.4 us, 3.7 TB/s; 30001 x 4096 (66 MB): 14.9 us,
+// 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.7 us, of which a launch is about four.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -28,6 +29,7 @@ namespace twell {
 
 namespace {
 
+typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -86,13 +88,13 @@ __device__ __forceinline__ u32x4 x_bf16(uint32_t lo, uint32_t hi, float scale) {
 // ---------------------------------------------------------------- the matrix path
 
 // The waves of a workgroup split K; each has RT tiles of 16 rows times TT tiles of
-// 16 tokens, and the registers of OCC workgroups a CU.
-template <bool MX_, int RT_, int TT_, int OCC_>
+// 16 tokens.  Up to WAVES waves, with the registers of OCC a SIMD.
+template <bool MX_, int RT_, int TT_, int WAVES_, int OCC_>
 struct Tile {
   static constexpr bool MX = MX_;
   static constexpr int RT = RT_, TT = TT_, ROWS = 16 * RT, TOKS = 16 * TT;
   static constexpr int E = RT * TT;                  // 16x16 results
-  static constexpr int OCC = OCC_;
+  static constexpr int WAVES = WAVES_, OCC = OCC_;
   static constexpr int XB = MX ? 128 : 256;          // bytes of a token's chunk
   static constexpr int XP = XB + 16;                 // and of its row in LDS: 16 tokens' same unit lies in all banks
   static constexpr int XL = XB * 16 / 1024;          // loads of a chunk of 16 tokens
@@ -119,31 +121,35 @@ __device__ __forceinline__ float scale_at(uint32_t s, int hi) {
   return __uint_as_float(__builtin_rotateright32(s, 9 + 8 * hi));
 }
 
-// Four scales of a row from block b on, a byte each (blocks past the row's end: its
-// last one, not used).
+// Four scales of a row from block b on, a byte each: loaded as the last four at most
+// and shifted into place when they are used, so that nothing waits for the load
+// before that.  Blocks past the row's end are not to be used.
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int b, int blocks) {
-  uint32_t v;
-  if (blocks % 4 == 0) {
-    memcpy(&v, p + min(b, blocks - 4), 4);
+  uint32_t v = 0;
+  if (blocks >= 4) {
+    v = *(const u32_any*)(p + min(b, blocks - 4));
   } else {
-    const uint32_t v0 = p[min(b, blocks - 1)], v1 = p[min(b + 1, blocks - 1)];
-    const uint32_t v2 = p[min(b + 2, blocks - 1)], v3 = p[min(b + 3, blocks - 1)];
-    v = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v |= (uint32_t)p[min(i, blocks - 1)] << (8 * i);
   }
   return v;
+}
+__device__ __forceinline__ uint32_t scales_at(uint32_t v, int b, int blocks) {
+  return v >> (8 * (b - min(b, max(blocks - 4, 0))) & 31);
 }
 
 // Sums over K of 16 RT rows (row(i): the row of W behind row i) and the tokens from
 // t0: wave w of `waves` gets results e = w, w + waves, ... of index r * TT + t in
 // out(e, sum); lane l's register i is row 4 (l / 16) + i of token l % 16.
-// Whole groups of K go round the waves, and then the chunks past them.
+// Each wave takes a run of K's chunks, in pieces of four (their scales are one load).
 template <class C, class Row, class Out>
 __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, Row row, int t0, char* lds, Out out) {
   constexpr int RT = C::RT, TT = C::TT, XL = C::XL;
   constexpr bool MX = C::MX;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int lo = lane & 15, hi = lane >> 4;
-  const int blocks = a.K / 32, groups = a.K / GROUP, chunks = (blocks + 3) / 4;
+  const int blocks = a.K / 32, chunks = (blocks + 3) / 4;
+  const int c0 = chunks * w / waves, c1 = chunks * (w + 1) / waves;      // this wave's
   WaveLds<C>& my = *(WaveLds<C>*)(lds + w * sizeof(WaveLds<C>));
   // This lane's addresses: a block of a chunk and a chunk's scales of row lane / 4,
   // and 16 bytes of a token of each load.
@@ -225,97 +231,60 @@ __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, R
     }
   };
 
-  if (w < groups) {
-    u32x4 wf[RT], xf[TT][XL];                        // one chunk in flight: more cost waves
+  if (c0 < c1) {
+    u32x4 wf[RT], xf[TT][XL];                        // one chunk in flight: with more the registers do not last
     uint32_t sf[RT], xsf[TT] = {};
-    const int wo = (lane & 3) * 16;
-    auto load = [&](int ck) {
+    auto load = [&](int ck) {                        // blocks past the row's end: its last one, not used
+      const int wo = min(ck * 64 + (lane & 3) * 16, blocks * 16 - 16), xo = min(ck * C::XB + xu, blocks * (C::XB / 4) - 16);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) wf[r] = *(const u32x4*)(wp[r] + ck * 64 + wo);
+      for (int r = 0; r < RT; ++r) wf[r] = *(const u32x4*)(wp[r] + wo);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < XL; ++i) xf[t][i] = load16(xp[t][i] + ck * C::XB + xu);
+        for (int i = 0; i < XL; ++i) xf[t][i] = load16(xp[t][i] + xo);
     };
-    auto load_group_scales = [&](int g) {
+    auto load_piece_scales = [&](int ck) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) sf[r] = load_scales(sp[r], g * 16 + (lane & 3) * 4, blocks);
+      for (int r = 0; r < RT; ++r) sf[r] = load_scales(sp[r], (ck + (lane & 3)) * 4, blocks);
       if constexpr (MX) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) xsf[t] = load_scales(xsp[t], g * 16 + (lane & 3) * 4, blocks);
+        for (int t = 0; t < TT; ++t) xsf[t] = load_scales(xsp[t], (ck + (lane & 3)) * 4, blocks);
       }
     };
-    load_group_scales(w);
-    load(4 * w);
+    load_piece_scales(c0);
+    load(c0);
+    // Not unrolled: a short call runs this code once or twice, and instructions that
+    // are not in the cache yet cost more than the loop's few.
 #pragma unroll 1
-    for (int g = w; g < groups; g += waves) {
+    for (int ck = c0; ck < c1; ++ck) {
+      const int p = (ck - c0) & 3;
+      if (p == 0) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) my.s[r][lane] = sf[r];
-      if constexpr (MX) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t) my.xs[t][lane] = xsf[t];
-      }
-      u32x4 sc[RT], xsc[TT];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) *(u32x4*)(ww + 16 * r * WP) = wf[r];
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = xf[t][i];
-        wave_lds_fence();
-        if (c == 0) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r) sc[r] = *(const u32x4*)&my.s[r][4 * lo];
-          if constexpr (MX) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) xsc[t] = *(const u32x4*)&my.xs[t][4 * lo];
-          }
-        }
-        if (c < 3) {
-          load(4 * g + c + 1);
-        } else if (g + waves < groups) {
-          load_group_scales(g + waves);
-          load(4 * (g + waves));
-        }
-        uint32_t s[RT], xs[TT] = {};
-#pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = sc[r][c];
+        for (int r = 0; r < RT; ++r) my.s[r][lane] = scales_at(sf[r], (ck + (lane & 3)) * 4, blocks);
         if constexpr (MX) {
 #pragma unroll
-          for (int t = 0; t < TT; ++t) xs[t] = xsc[t][c];
+          for (int t = 0; t < TT; ++t) my.xs[t][lane] = scales_at(xsf[t], (ck + (lane & 3)) * 4, blocks);
         }
-        multiply(s, xs, 4);
-        wave_lds_fence();
       }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) *(u32x4*)(ww + 16 * r * WP) = wf[r];
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = xf[t][i];
+      wave_lds_fence();
+      if (ck + 1 < c1) load(ck + 1);
+      if (p == 0 && ck + 4 < c1) load_piece_scales(ck + 4);
+      uint32_t s[RT], xs[TT] = {};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r] = my.s[r][4 * lo + p];
+      if constexpr (MX) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) xs[t] = my.xs[t][4 * lo + p];
+      }
+      multiply(s, xs, blocks - 4 * ck);
+      wave_lds_fence();
     }
-  }
-#pragma unroll 1
-  for (int ck = groups * 4 + w; ck < chunks; ck += waves) {
-    uint32_t s[RT], xs[TT] = {};
-    const int wo = min(ck * 4 + (lane & 3), blocks - 1) * 16, xo = min(ck * C::XB + xu, blocks * (C::XB / 4) - 16);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      *(u32x4*)(ww + 16 * r * WP) = *(const u32x4*)(wp[r] + wo);
-      my.s[r][lane] = load_scales(sp[r], ck * 4, blocks);
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-#pragma unroll
-      for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = load16(xp[t][i] + xo);
-      if constexpr (MX) my.xs[t][lane] = load_scales(xsp[t], ck * 4, blocks);
-    }
-    wave_lds_fence();
-    // load_scales starts at the last four blocks where they are whole chunks, so at ck's
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s[r] = my.s[r][4 * lo];
-    if constexpr (MX) {
-#pragma unroll
-      for (int t = 0; t < TT; ++t) xs[t] = my.xs[t][4 * lo];
-    }
-    multiply(s, xs, blocks - 4 * ck);
-    wave_lds_fence();
   }
   __syncthreads();                                   // the sums lie over the waves' pieces
   f32x4 (*sum)[C::E][64] = (f32x4(*)[C::E][64])lds;
@@ -339,13 +308,12 @@ __device__ __forceinline__ f32x4 bias4(const W4Args& a, int64_t n) {
   return b;
 }
 
-constexpr int TILE_WAVES = 4;
 extern __shared__ __attribute__((aligned(16))) char dyn_lds[];
 
 }  // namespace
 
 template <class C>
-__global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_matvec_kernel(W4Args a) {
+__global__ __launch_bounds__(64 * C::WAVES, C::OCC) void w4_matvec_kernel(W4Args a) {
   const int lane = threadIdx.x & 63;
   const int64_t n0 = (int64_t)blockIdx.x * C::ROWS;
   for (int t0 = blockIdx.y * C::TOKS; t0 < a.T; t0 += gridDim.y * C::TOKS) {
@@ -381,12 +349,14 @@ __global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_matvec_kernel(W4Ar
 
 // The layer's gate and up products of a workgroup's neurons: g = x . Wg^T + bg;
 // where a neuron fires (g > 0) for some token of the workgroup, u = x . Wu^T on the
-// neurons that fire, listed, and a = g u is stored for the pairs that do, with a bit
-// for each pair.  Other rows of Wu are not read.  F is a multiple of the
+// neurons that fire, listed, 16 at a time, and a = g u is stored for the pairs that
+// do, with a bit for each pair.  Other rows of Wu are not read.  (One pair after the
+// other, without the tile: the few neurons that fire for many tokens hold their
+// workgroup up; 64 tokens at 2048 x 5632, 21.6 us and 17.9.)  F is a multiple of the
 // workgroup's rows.
 template <class C>
-__global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_gate_up_kernel(W4Args a) {
-  using U = Tile<C::MX, 1, C::TT, C::OCC>;
+__global__ __launch_bounds__(64 * C::WAVES, C::OCC) void w4_gate_up_kernel(W4Args a) {
+  using U = Tile<C::MX, 1, C::TT, C::WAVES, C::OCC>;
   __shared__ uint32_t fires[C::RT];                  // of each tile of 16 rows
   __shared__ float hl[C::TOKS][C::ROWS + 1];         // max(g, 0), NaN as 0
   __shared__ int list[C::ROWS];                      // the rows that fire
@@ -419,28 +389,28 @@ __global__ __launch_bounds__(64 * TILE_WAVES, C::OCC) void w4_gate_up_kernel(W4A
       count += __builtin_popcount(m);
     }
     __syncthreads();
-    auto up = [&](auto tile) {
-      using V = decltype(tile);
-      tile_product<V>(
-          a, a.Wu, [&](int i) { return (int64_t)(n0 + list[min(i, count - 1)]); }, t0, dyn_lds, [&](int e, f32x4 u) {
-            const int tl = 16 * (e % V::TT) + (lane & 15);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += 16) {
+      tile_product<U>(
+          a, a.Wu, [&](int i) { return (int64_t)(n0 + list[min(k0 + i, count - 1)]); }, t0, dyn_lds,
+          [&](int e, f32x4 u) {
+            const int tl = 16 * (e % U::TT) + (lane & 15);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int k = 16 * (e / V::TT) + 4 * (lane >> 4) + i;
+              const int k = k0 + 4 * (lane >> 4) + i;
               if (k < count) {
                 const float h = hl[tl][list[k]];
                 if (h > 0.f) a.act[(int64_t)(t0 + tl) * a.N + n0 + list[k]] = h * u[i];
               }
             }
           });
-    };
-    if (count > 16) up(C{});
-    else if (count > 0) up(U{});
+      __syncthreads();                             // the next tile lies over its sums
+    }
     __syncthreads();
   }
 }
 
-// ---------------------------------------------------------------- up to four tokens
+// ---------------------------------------------------------------- one and two tokens
 
 namespace {
 
@@ -697,21 +667,28 @@ __global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
 
 namespace {
 
-// Calls f with the tile for the tokens and rows: 32 rows x 16 tokens, the most
-// workgroups and waves, unless there are enough workgroups of 64 x 32, which read
-// the tokens half as often (64 tokens: 40001 x 2048, 29 us and 42 with the small
-// tile; 5632 x 2048, 8.0 and 7.4).
+// Calls f with the tile for the tokens and rows: 32 rows x 16 tokens, unless there
+// are enough workgroups of 64 x 32 (of a product; the layer's list of rows that fire
+// grows with both), which read the tokens half as often, or there is no more than
+// one of 16 x 16 for each CU.  With the other tile: 64 tokens, 40001 x 2048, 26 us and
+// 42 (small); 9216 x 2304, 11.5 and 13 (large) and 20.8 (narrow); 30 tokens, 700 x
+// 8192, 6.2 and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0 (narrow).
 template <bool MX>
-using Small = Tile<MX, 2, 1, 3>;
+using Narrow = Tile<MX, 1, 1, 8, 4>;
 template <bool MX>
-using Large = Tile<MX, 4, 2, 2>;
-template <class F>
+using Small = Tile<MX, 2, 1, 8, 3>;
+template <bool MX>
+using Large = Tile<MX, 4, 2, 4, 2>;
+template <bool PRODUCT, class F>
 void with_tile(const W4Args& a, F f) {
-  const bool large = a.T > 16 && a.N > 16384;
-  if (a.x_scale && large) f(Large<true>{});
-  else if (a.x_scale) f(Small<true>{});
-  else if (large) f(Large<false>{});
-  else f(Small<false>{});
+  auto go = [&](auto mx) {
+    if constexpr (PRODUCT)
+      if (a.T > 16 && a.N > 16384) return f(Large<mx.value>{});
+    if ((int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256) f(Narrow<mx.value>{});
+    else f(Small<mx.value>{});
+  };
+  if (a.x_scale) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 // Waves of a workgroup: one per group of K, up to `most`.
@@ -726,6 +703,22 @@ template <class C>
 dim3 tile_grid(const W4Args& a) {
   const int toks = (a.T + C::TOKS - 1) / C::TOKS;
   return dim3((a.N + C::ROWS - 1) / C::ROWS, toks < TOKEN_GRID ? toks : TOKEN_GRID);
+}
+
+// The same of the matrix path: one per four chunks where workgroups are many (the
+// waves' sums go through LDS at the end), otherwise one per chunk; up to four, and to
+// eight where there is no more than a workgroup for each CU and K is long.  9 tokens,
+// 3001 x 480: 3.2 us, and 4.0 with one per four; 64 tokens, 65536 x 512: 19.9 and 15.7;
+// 5 tokens, 5000 x 16384: 13.2, and 17.1 with four; 64 tokens, 9216 x 2304: 14.6 and
+// 11.5.
+template <class C>
+int tile_waves(const W4Args& a) {
+  const dim3 g = tile_grid<C>(a);
+  const int64_t groups = (int64_t)g.x * g.y;
+  const int chunks = (a.K + CHUNK - 1) / CHUNK;
+  const int waves = C::TT > 1 || groups > 1024 ? (chunks + 3) / 4 : chunks;
+  const int most = C::WAVES > 4 && groups <= 256 && (C::RT == 1 || chunks >= 32) ? 8 : 4;
+  return waves < most ? waves : most;
 }
 
 bool use_gemv(const W4Args& a) { return a.T <= GEMV_T; }
@@ -746,9 +739,9 @@ hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s) {
       w4_gemv_kernel<t.value><<<dim3((a.N + GEMV_ROWS - 1) / GEMV_ROWS), threads, 0, s>>>(a);
     });
   } else {
-    with_tile(a, [&](auto c) {
+    with_tile<true>(a, [&](auto c) {
       using C = decltype(c);
-      w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
+      w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * tile_waves<C>(a), tile_lds<C>(tile_waves<C>(a)), s>>>(a);
     });
   }
   return hipGetLastError();
@@ -767,12 +760,10 @@ hipError_t launch_ffn_w4(W4Args a, void* ws, hipStream_t s) {
       w4_gate_up_gemv_kernel<t.value><<<dim3(a.N / GEMV_ROWS), threads, 0, s>>>(a);
     });
   } else {
-    auto go = [&](auto c) {
+    with_tile<false>(a, [&](auto c) {
       using C = decltype(c);
-      w4_gate_up_kernel<C><<<tile_grid<C>(a), 64 * waves_of(a, TILE_WAVES), tile_lds<C>(waves_of(a, TILE_WAVES)), s>>>(a);
-    };
-    if (a.x_scale) go(Small<true>{});
-    else go(Small<false>{});
+      w4_gate_up_kernel<C><<<tile_grid<C>(a), 64 * tile_waves<C>(a), tile_lds<C>(tile_waves<C>(a)), s>>>(a);
+    });
   }
   w4_down_kernel<<<dim3((a.K + DB * 32 - 1) / (DB * 32), a.T < TOKEN_GRID ? a.T : TOKEN_GRID), DB * NS, 0, s>>>(a);
   return hipGetLastError();

@@ -593,7 +593,7 @@ twell_status twell_dropout_add(const twell_norm_shape *sh, const void *x, int64_
  * Serving on 4-bit weights
  * ---------------------------------------------------------------------------
  *
- * A weight matrix [N][K] in MXFP4 (K % 32 == 0): e2m1 values (1 sign, 2
+ * A weight matrix [N][K] in MXFP4 (K % 32 == 0, K < 2^30): e2m1 values (1 sign, 2
  * exponent and 1 mantissa bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale per 32
  * columns of a row.
  *   codes   uint8 [N][K / 2]   two values a byte, the even column in the low

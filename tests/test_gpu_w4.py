@@ -343,3 +343,18 @@ def test_layer_repeats_on_a_stream_and_in_a_graph(torch, tw, kind):
         step()
         torch.cuda.synchronize()
         assert torch.equal(y, got[0]) and torch.equal(z, got[1]), k
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 4500, 4192), (33, 2200, 4128), (3, 8200, 4096), (20, 17000, 96), (3, 4200, 64),
+                                   (50, 300, 8288), (9, 33000, 672), (16, 4097, 32)])
+@pytest.mark.parametrize("kind", ["bf16", "mx8"])
+def test_matvec_splits(torch, tw, T, N, K, kind):
+    """The splits of K over a workgroup's waves: one to eight of them, runs of
+    chunks that are no multiple of four, and rows of fewer than four blocks."""
+    r = np.random.default_rng(T + N + K)
+    W, w = make_w(torch, tw, r, N, K, K ** -0.5)
+    x, xs, xv = make_x(torch, r, T, K, kind)
+    log(f"[w4 splits] T={T} N={N} K={K} {kind}")
+    y = out(torch, T, N, "f32")
+    tw.twell_w4_matvec(x, xs, W, None, y)
+    check_product(values(y), xv, w, None, "f32")

@@ -98,3 +98,7 @@ def test_binding_checks_tensors():
             tw.twell_w4_matvec(*args)
     with pytest.raises(TypeError):
         tw.twell_w4_matvec(x, None, W, b, y.double())
+
+
+def test_matvec_refuses_rows_past_32_bit_offsets():
+    assert _matvec(_w(K=1 << 30), ldx=1 << 30) == tw.TWELL_EUNSUPPORTED
