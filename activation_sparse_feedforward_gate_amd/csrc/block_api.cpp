@@ -43,9 +43,11 @@ twell_status mat(RowMat* m, const twell_norm_shape* sh, const void* p, int64_t l
   return TWELL_OK;
 }
 
-twell_status weights(NormArgs* a, const twell_norm_shape* sh, const void* w) {
-  a->w = w;
-  a->w_dt = sh->w_dt;
+// The norm's weights; row: a row of type row_dt that stands in where there are none.
+twell_status weights(NormArgs* a, const twell_norm_shape* sh, const void* w, const void* row, int row_dt) {
+  a->w = w ? w : row;
+  a->w_dt = w ? (int)sh->w_dt : row_dt;
+  a->w_given = w != nullptr;
   if ((uintptr_t)w % dt_size(sh->w_dt)) return FAIL(TWELL_EINVAL, "w is not aligned to its elements");
   return TWELL_OK;
 }
@@ -108,7 +110,7 @@ twell_status twell_add_rmsnorm_fwd(const twell_norm_shape* sh, const void* x, in
   CHECK(mat(&a.res, sh, residual, ldres, sh->res_dt, "residual"));
   CHECK(mat(&a.sum, sh, sum, ldsum, sh->res_dt, "sum"));
   CHECK(mat(&a.y, sh, y, ldy, sh->y_dt, "y"));
-  CHECK(weights(&a, sh, w));
+  CHECK(weights(&a, sh, w, x, sh->x_dt));
   CHECK(dropout(&a, sh, rng));
   if (!x || !y) return FAIL(TWELL_EINVAL, "NULL tensor argument");
   if (!sum && (residual || a.drop)) return FAIL(TWELL_EINVAL, "sum is required with a residual or dropout");
@@ -136,7 +138,7 @@ twell_status twell_add_rmsnorm_bwd(const twell_norm_shape* sh, const void* dy, i
   CHECK(mat(&a.sum, sh, sum, ldsum, sh->res_dt, "sum"));
   CHECK(mat(&a.dres, sh, dres, lddres, sh->res_dt, "dres"));
   CHECK(mat(&a.x, sh, dx, lddx, sh->x_dt, "dx"));
-  CHECK(weights(&a, sh, w));
+  CHECK(weights(&a, sh, w, sum, sh->res_dt));
   CHECK(dropout(&a, sh, rng));
   if (sh->T > 0 && (!dy || !sum || !rstd || (!dres && !dx))) return FAIL(TWELL_EINVAL, "NULL tensor argument");
   if ((uintptr_t)rstd % 4 || (uintptr_t)dw % 4) return FAIL(TWELL_EINVAL, "rstd or dw is not aligned to its elements");

@@ -33,14 +33,45 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
   return v;
 }
 
-__device__ __forceinline__ void load_w(const NormArgs& a, int c, float w[8]) {
-  if (!a.w) {
+// Eight of the norm's weights as loaded, of either type, with no branch (they are
+// loaded with the row, ahead of its sum): two 16-byte loads, of which bf16 needs the
+// first.
+template <bool SHORT>
+struct RawW {
+  uint32_t u[8];
+};
+template <bool SHORT>
+__device__ __forceinline__ RawW<SHORT> load_w(const NormArgs& a, int c) {
+  RawW<SHORT> r;
+  if constexpr (SHORT) {
+    if (a.w_dt == DT_F32) {
+      const Raw8<f32_t> q = load_raw<f32_t>(a.w, c, a.d - c);
+      memcpy(r.u, q.u, 32);
+    } else {
+      const Raw8<bf16_t> q = load_raw<bf16_t>(a.w, c, a.d - c);
+      memcpy(r.u, q.u, 16);
+    }
+  } else {
+    const bool f = a.w_dt == DT_F32;
+    const char* p = (const char*)a.w + ((int64_t)min(c, a.d - 8) << (f ? 2 : 1));
+    memcpy(r.u, p, 16);
+    memcpy(r.u + 4, p + (f ? 16 : 0), 16);
+  }
+  return r;
+}
+template <bool SHORT>
+__device__ __forceinline__ void w_values(const NormArgs& a, const RawW<SHORT>& r, int c, float w[8]) {
+  if (!a.w_given) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f;
   } else if (a.w_dt == DT_F32) {
-    chunk_values(load_chunk<f32_t>(a.w, c, a.d), c, a.d, w);
+    Raw8<f32_t> q;
+    memcpy(q.u, r.u, 32);
+    chunk_values<f32_t, SHORT>(q, c, a.d, w);
   } else {
-    chunk_values(load_chunk<bf16_t>(a.w, c, a.d), c, a.d, w);
+    Raw8<bf16_t> q;
+    memcpy(q.u, r.u, 16);
+    chunk_values<bf16_t, SHORT>(q, c, a.d, w);
   }
 }
 
@@ -92,7 +123,7 @@ constexpr int threads_of(int lpr) { return lpr < 256 ? 256 : lpr; }
 
 }  // namespace
 
-template <class X, class R, class Y, int LPR, int CH>
+template <class X, class R, class Y, int LPR, int CH, bool SHORT>
 __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
   __shared__ float sh[threads_of(LPR) / 64];
   constexpr int RPB = threads_of(LPR) / LPR;
@@ -114,15 +145,18 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * LPR + lane) * 8;
-      xv[k] = load_chunk<X>(xr, c, a.d);
+      xv[k] = load_chunk<X, SHORT>(xr, c, a.d);
     }
     if (a.res.p) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int c = (k * LPR + lane) * 8;
-        rv[k] = load_chunk<R>(rr, c, a.d);
+        rv[k] = load_chunk<R, SHORT>(rr, c, a.d);
       }
     }
+    RawW<SHORT> wv[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) wv[k] = load_w<SHORT>(a, (k * LPR + lane) * 8);
     float v[CH][8], sq = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -130,11 +164,11 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
       if (c < a.d) {
-        chunk_values(xv[k], c, a.d, v[k]);
+        chunk_values<X, SHORT>(xv[k], c, a.d, v[k]);
         if (a.drop) dropout8(g, t * nb + (c >> 3), a.drop, a.keep_scale, v[k]);
         if (a.res.p) {
           float r[8];
-          chunk_values(rv[k], c, a.d, r);
+          chunk_values<R, SHORT>(rv[k], c, a.d, r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[k][i] += r[i];
         }
@@ -154,7 +188,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
       const int c = (k * LPR + lane) * 8;
       float w[8];
       if (c < a.d) {
-        load_w(a, c, w);
+        w_values(a, wv[k], c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * rstd * w[i];
       }
@@ -166,7 +200,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
 
 // The rows are dealt out to gridDim.x workgroups; each leaves its rows' part
 // of dw in its row of `part`.
-template <class Y, class R, class X, int LPR, int CH>
+template <class Y, class R, class X, int LPR, int CH, bool SHORT>
 __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int NTH = threads_of(LPR), RPB = NTH / LPR;
   __shared__ float sh[RPB > 1 ? 8 * NTH : NTH / 64];
@@ -175,6 +209,9 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
   if (a.drop) g.load(a.rng);
   const int nb = (a.d + 7) / 8;
   float dw[CH][8] = {};
+  RawW<SHORT> wv[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) wv[k] = load_w<SHORT>(a, (k * LPR + lane) * 8);
   for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB) {
     int64_t t = t0 + threadIdx.x / LPR;
     const bool live = t < a.T;
@@ -186,14 +223,14 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * LPR + lane) * 8;
-      yv[k] = load_chunk<Y>(yr, c, a.d);
-      sv[k] = load_chunk<R>(sr, c, a.d);
+      yv[k] = load_chunk<Y, SHORT>(yr, c, a.d);
+      sv[k] = load_chunk<R, SHORT>(sr, c, a.d);
     }
     if (a.res.p) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int c = (k * LPR + lane) * 8;
-        ds[k] = load_chunk<R>(row_of<R>(a.res, t), c, a.d);
+        ds[k] = load_chunk<R, SHORT>(row_of<R>(a.res, t), c, a.d);
       }
     }
     const float rstd = a.rstd_in[t];
@@ -204,9 +241,9 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
       const int c = (k * LPR + lane) * 8;
       if (c < a.d) {
         float v[8], w[8];
-        chunk_values(yv[k], c, a.d, gy[k]);
-        chunk_values(sv[k], c, a.d, v);
-        load_w(a, c, w);
+        chunk_values<Y, SHORT>(yv[k], c, a.d, gy[k]);
+        chunk_values<R, SHORT>(sv[k], c, a.d, v);
+        w_values(a, wv[k], c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {                          // columns past d: 0 * 0
           const float xh = v[i] * rstd;
@@ -223,8 +260,8 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
         const int c = (k * LPR + lane) * 8, n = a.d - c;
         if (n > 0) {
           float v[8], o[8] = {};
-          chunk_values(sv[k], c, a.d, v);
-          if (a.res.p) chunk_values(ds[k], c, a.d, o);
+          chunk_values<R, SHORT>(sv[k], c, a.d, v);
+          if (a.res.p) chunk_values<R, SHORT>(ds[k], c, a.d, o);
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] += rstd * (gy[k][i] - v[i] * rstd * cm);
           if (a.dres.p) store8<R>(row_of<R>(a.dres, t), c, n, o);
@@ -279,7 +316,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormArgs a) {
       float dy[8], v[8], w[8];
       load8<Y>(yr, c, n, dy);
       load8<R>(sr, c, n, v);
-      load_w(a, c, w);
+      w_values(a, load_w<false>(a, c), c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < n) dot += dy[i] * w[i] * (v[i] * rstd);
@@ -290,7 +327,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormArgs a) {
       float dy[8], v[8], w[8], ds[8] = {}, p[8] = {};
       load8<Y>(yr, c, n, dy);
       load8<R>(sr, c, n, v);
-      load_w(a, c, w);
+      w_values(a, load_w<false>(a, c), c, w);
       if (a.res.p) load8<R>(row_of<R>(a.res, t), c, n, ds);
       if (part && t != blockIdx.x) load8<f32_t>(part, c, n, p);
 #pragma unroll
@@ -331,7 +368,7 @@ __global__ __launch_bounds__(DW_COLS * DW_ROWS) void norm_dw_kernel(const float*
 // rpb rows a workgroup where a row has fewer than 256 chunks of eight columns,
 // otherwise one.
 constexpr int DROP_NTH = 256;
-template <class X, class R, class Y>
+template <class X, class R, class Y, bool SHORT>
 __global__ __launch_bounds__(DROP_NTH) void dropout_add_kernel(NormArgs a, int rpb) {
   Philox g{};
   if (a.drop) g.load(a.rng);
@@ -342,13 +379,13 @@ __global__ __launch_bounds__(DROP_NTH) void dropout_add_kernel(NormArgs a, int r
     for (int b = rpb > 1 ? threadIdx.x % nb : threadIdx.x; b < nb; b += DROP_NTH) {
       const int c = 8 * b;
       float v[8], r[8];
-      const Raw8<X> xv = load_chunk<X>(row_of<X>(a.x, t), c, a.d);
+      const Raw8<X> xv = load_chunk<X, SHORT>(row_of<X>(a.x, t), c, a.d);
       Raw8<R> rv;
-      if (a.res.p) rv = load_chunk<R>(row_of<R>(a.res, t), c, a.d);
-      chunk_values(xv, c, a.d, v);
+      if (a.res.p) rv = load_chunk<R, SHORT>(row_of<R>(a.res, t), c, a.d);
+      chunk_values<X, SHORT>(xv, c, a.d, v);
       if (a.drop) dropout8(g, t * nb + b, a.drop, a.keep_scale, v);
       if (a.res.p) {
-        chunk_values(rv, c, a.d, r);
+        chunk_values<R, SHORT>(rv, c, a.d, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += r[i];
       }
@@ -371,8 +408,9 @@ void with_types(int a, int b, int c, F f) {
 constexpr int64_t ROW_GRID = 1 << 20;    // workgroups of a launch; more rows are walked in a loop
 
 // Lanes per row and chunks per lane.
-template <int LPR_, int CH_>
+template <int LPR_, int CH_, bool SHORT_ = false>
 struct Cfg {
+  static constexpr bool SHORT = SHORT_;
   static constexpr int LPR = LPR_, CH = CH_, RPB = threads_of(LPR_) / LPR_;
 };
 
@@ -384,6 +422,7 @@ struct Cfg {
 // 5.2; 1024 rows, 7.7, 6.5 and 6.9.
 template <class F>
 void with_fwd_cfg(int T, int d, F f) {
+  if (d < 8) return f(Cfg<16, 1, true>{});
   if (T <= 512 && d > 512) {
     if (d <= 2048) return f(Cfg<256, 1>{});
     if (d <= 4096) return f(Cfg<512, 1>{});
@@ -409,6 +448,7 @@ void with_fwd_cfg(int T, int d, F f) {
 constexpr int BWD_MAX_D = 16384;
 template <class F>
 void with_bwd_cfg(int d, F f) {
+  if (d < 8) return f(Cfg<16, 1, true>{}, 1280);
   if (d <= 128) return f(Cfg<16, 1>{}, 1280);
   if (d <= 256) return f(Cfg<32, 1>{}, 1280);
   if (d <= 512) return f(Cfg<64, 1>{}, 1280);
@@ -428,8 +468,8 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
       using C = decltype(c);
       const int64_t blocks = ((int64_t)a.T + C::RPB - 1) / C::RPB;
       const dim3 grid((unsigned)(blocks < ROW_GRID ? blocks : ROW_GRID));
-      if (a.y.dt == DT_MXFP8) norm_fwd_kernel<X, R, mx8_t, C::LPR, C::CH><<<grid, threads_of(C::LPR), 0, s>>>(a);
-      else norm_fwd_kernel<X, R, Y, C::LPR, C::CH><<<grid, threads_of(C::LPR), 0, s>>>(a);
+      if (a.y.dt == DT_MXFP8) norm_fwd_kernel<X, R, mx8_t, C::LPR, C::CH, C::SHORT><<<grid, threads_of(C::LPR), 0, s>>>(a);
+      else norm_fwd_kernel<X, R, Y, C::LPR, C::CH, C::SHORT><<<grid, threads_of(C::LPR), 0, s>>>(a);
     });
   });
   return hipGetLastError();
@@ -453,7 +493,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
       if (a.d > BWD_MAX_D) return norm_bwd_wide_kernel<Y, R, X><<<dim3(parts), WIDE, 0, s>>>(a);
       with_bwd_cfg(a.d, [&](auto c, int) {
         using C = decltype(c);
-        norm_bwd_kernel<Y, R, X, C::LPR, C::CH><<<dim3(parts), threads_of(C::LPR), 0, s>>>(a);
+        norm_bwd_kernel<Y, R, X, C::LPR, C::CH, C::SHORT><<<dim3(parts), threads_of(C::LPR), 0, s>>>(a);
       });
     });
   if (a.dw) norm_dw_kernel<<<dim3((a.d + DW_COLS - 1) / DW_COLS), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
@@ -465,7 +505,9 @@ hipError_t launch_dropout_add(const NormArgs& a, hipStream_t s) {
   const int64_t blocks = ((int64_t)a.T + rpb - 1) / rpb;
   const dim3 grid((unsigned)(blocks < ROW_GRID ? blocks : ROW_GRID));
   with_types(a.x.dt, a.res.dt, a.y.dt, [&](auto x, auto r, auto y) {
-    dropout_add_kernel<decltype(x), decltype(r), decltype(y)><<<grid, DROP_NTH, 0, s>>>(a, rpb);
+    using X = decltype(x); using R = decltype(r); using Y = decltype(y);
+    if (a.d < 8) dropout_add_kernel<X, R, Y, true><<<grid, DROP_NTH, 0, s>>>(a, rpb);
+    else dropout_add_kernel<X, R, Y, false><<<grid, DROP_NTH, 0, s>>>(a, rpb);
   });
   return hipGetLastError();
 }

@@ -251,8 +251,9 @@ struct NormArgs {
   int T, d;
   RowMat x, res, sum, y;     // forward; backward: x = dx, res = dsum, sum, y = dy, dres
   RowMat dres;
-  const void* w;             // null: ones
+  const void* w;             // ones where not given, and then any memory of a row's size
   int w_dt;
+  bool w_given;
   uint8_t* y_scale;          // MXFP8 y
   float* rstd;
   const float* rstd_in;      // backward

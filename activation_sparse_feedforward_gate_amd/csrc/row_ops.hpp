@@ -70,16 +70,16 @@ __device__ __forceinline__ void load8(const void* row, int c0, int n, float v[8]
 // them: one whole load at min(c, d - 8), with no branch (a branch per chunk ends
 // in a wait for its loads), and the ragged last chunk of a row is shifted into
 // place when it is used.  Chunks past the row's end load its last columns and
-// are not to be used.
-template <class E>
+// are not to be used.  SHORT: rows of fewer than eight columns, one chunk in all.
+template <class E, bool SHORT>
 __device__ __forceinline__ Raw8<E> load_chunk(const void* row, int c, int d) {
-  if (d < 8) return load_raw<E>(row, c, d - c);      // one chunk in all
-  return load_raw<E>(row, min(c, d - 8), 8);
+  if constexpr (SHORT) return load_raw<E>(row, c, d - c);
+  else return load_raw<E>(row, min(c, d - 8), 8);
 }
-template <class E>
+template <class E, bool SHORT>
 __device__ __forceinline__ void chunk_values(const Raw8<E>& r, int c, int d, float v[8]) {
   r.values(v);
-  if (d % 8 && d > 8) {
+  if (!SHORT && d % 8) {
     const int miss = c - min(c, d - 8);
 #pragma unroll
     for (int k = 4; k; k >>= 1)
