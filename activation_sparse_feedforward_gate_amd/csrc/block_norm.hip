@@ -198,12 +198,61 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
   }
 }
 
-// The rows are dealt out to gridDim.x workgroups; each leaves its rows' part
-// of dw in its row of `part`.
+// Rows of 32 columns of dw by a workgroup of its own, from dy, sum and rstd alone:
+// 8 columns a thread, its rows added in order and the threads' sums after them.
+constexpr int DW_COLS = 32;
+template <class Y, class R, int NTH>
+__device__ __forceinline__ void dw_columns(const NormArgs& a, int c0, float* sh) {
+  constexpr int TPR = DW_COLS / 8, ROWS = NTH / TPR, U = 4;
+  const int y = threadIdx.x / TPR, c = c0 + threadIdx.x % TPR * 8, cl = min(c, (a.d - 1) / 8 * 8);
+  float s[8] = {};
+  for (int64_t t0 = y; t0 < a.T; t0 += ROWS * U) {
+    Raw8<Y> yv[U];
+    Raw8<R> sv[U];
+    float r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = min(t0 + u * ROWS, (int64_t)a.T - 1);
+      yv[u] = load_chunk<Y, false>(row_of<Y>(a.y, t), cl, a.d);
+      sv[u] = load_chunk<R, false>(row_of<R>(a.sum, t), cl, a.d);
+      r[u] = a.rstd_in[t];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t0 + u * ROWS < a.T) {
+        float dy[8], v[8];
+        chunk_values<Y, false>(yv[u], cl, a.d, dy);
+        chunk_values<R, false>(sv[u], cl, a.d, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += dy[i] * (v[i] * r[u]);
+      }
+  }
+  // Threads of a column are added over the lanes of a wave and then over the waves.
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = TPR; o < 64; o <<= 1) s[i] += __shfl_xor(s[i], o);
+    if ((threadIdx.x & 63) < TPR) sh[threadIdx.x / 64 * DW_COLS + threadIdx.x % TPR * 8 + i] = s[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < DW_COLS && c0 + (int)threadIdx.x < a.d) {
+    float v = sh[threadIdx.x];
+    for (int w = 1; w < NTH / 64; ++w) v += sh[w * DW_COLS + threadIdx.x];
+    a.dw[c0 + threadIdx.x] = v;
+  }
+}
+
+// The rows are dealt out to the workgroups past the first a.dw_blocks, of which each
+// has some columns of dw; with dw_blocks 0 each leaves its rows' part of dw in its
+// row of `part`.
 template <class Y, class R, class X, int LPR, int CH, bool SHORT>
 __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int NTH = threads_of(LPR), RPB = NTH / LPR;
-  __shared__ float sh[RPB > 1 ? 8 * NTH : NTH / 64];
+  constexpr int ROW_SH = RPB > 1 ? 8 * NTH : NTH / 64, COL_SH = NTH / 64 * DW_COLS;
+  __shared__ float sh[ROW_SH > COL_SH ? ROW_SH : COL_SH];
+  if constexpr (!SHORT)
+    if ((int)blockIdx.x < a.dw_blocks) return dw_columns<Y, R, NTH>(a, blockIdx.x * DW_COLS, sh);
+  const int block = blockIdx.x - a.dw_blocks, blocks = gridDim.x - a.dw_blocks;
   const int lane = threadIdx.x % LPR;
   Philox g{};
   if (a.drop) g.load(a.rng);
@@ -212,7 +261,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
   RawW<SHORT> wv[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) wv[k] = load_w<SHORT>(a, (k * LPR + lane) * 8);
-  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB) {
+  for (int64_t t0 = (int64_t)block * RPB; t0 < a.T; t0 += (int64_t)blocks * RPB) {
     int64_t t = t0 + threadIdx.x / LPR;
     const bool live = t < a.T;
     t = live ? t : a.T - 1;
@@ -273,8 +322,8 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
       }
     }
   }
-  if (!a.dw) return;
-  float* part = a.part + (int64_t)blockIdx.x * a.d;
+  if (!a.part) return;
+  float* part = a.part + (int64_t)block * a.d;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     if constexpr (RPB > 1) {
@@ -305,7 +354,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormArgs a) {
   Philox g{};
   if (a.drop) g.load(a.rng);
   const int nb = (a.d + 7) / 8;
-  float* part = a.dw ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const char* yr = row_of<Y>(a.y, t);
     const char* sr = row_of<R>(a.sum, t);
@@ -348,7 +397,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormArgs a) {
 
 // dw = the parts, added in a fixed order: 32 columns a workgroup, 32 threads a
 // column.
-constexpr int DW_COLS = 32, DW_ROWS = 32;
+constexpr int DW_ROWS = 32;
 __global__ __launch_bounds__(DW_COLS * DW_ROWS) void norm_dw_kernel(const float* part, int parts, int d, float* dw) {
   __shared__ float sh[DW_ROWS][DW_COLS + 1];
   const int x = threadIdx.x % DW_COLS, y = threadIdx.x / DW_COLS, c = blockIdx.x * DW_COLS + x;
@@ -416,7 +465,7 @@ struct Cfg {
 
 // Few chunks per lane and few idle lanes: two or three chunks in flight per lane
 // fill the memory pipe, more cost registers and so waves.  32768 rows of 2304
-// (fp32 x, bf16 rest, dropout): <128, 3> 137 us (5.5 TB/s), <256, 2> 144, <64, 5>
+// (fp32 x, bf16 rest, dropout): <128, 3> 129 us (5.8 TB/s), <256, 2> 144, <64, 5>
 // 166, <64, 8> 273.  Up to 512 rows the time is one row's latency and one chunk
 // a lane is fastest: 1 row of 2304 to MXFP8, <512, 1> 3.5 us, <256, 2> 4.2, <128, 3>
 // 5.2; 1024 rows, 7.7, 6.5 and 6.9.
@@ -475,6 +524,14 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Whether dw comes from workgroups of its own: they read dy and sum again, and save the
+// second launch (about 3 us) and the parts.  Rows 1 of 2304: 3.7 us, 7.2 by parts; 500
+// of 4096: 8.7 and 12.4; 777 of 1001 fp32: 9.6 and 10.3; 1024 of 2304: 11.6 and 12.5;
+// 1000 of 8000: 26.6 and 22.4; 2000 of 512: 11.1 and 9.1.
+bool dw_apart(const NormArgs& a) {
+  return a.d >= 8 && a.d <= BWD_MAX_D && a.T <= 1024 && (int64_t)a.T * a.d <= 4 << 20;
+}
+
 int norm_bwd_parts(int T, int d) {
   int64_t blocks = T, most = 512;
   if (d <= BWD_MAX_D)
@@ -485,18 +542,23 @@ int norm_bwd_parts(int T, int d) {
   return (int)(blocks < most ? blocks : most);
 }
 
-hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
-  const int parts = norm_bwd_parts(a.T, a.d);
+hipError_t launch_norm_bwd(NormArgs a, hipStream_t s) {
+  const int parts = norm_bwd_parts(a.T, a.d), dw_blocks = (a.d + DW_COLS - 1) / DW_COLS;
+  if (!a.dw) a.part = nullptr;
+  if (a.dw && a.T > 0 && dw_apart(a)) {
+    a.dw_blocks = dw_blocks;
+    a.part = nullptr;
+  }
   if (a.T > 0)
     with_types(a.y.dt, a.res.dt, a.x.dt, [&](auto y, auto r, auto x) {
       using Y = decltype(y); using R = decltype(r); using X = decltype(x);
       if (a.d > BWD_MAX_D) return norm_bwd_wide_kernel<Y, R, X><<<dim3(parts), WIDE, 0, s>>>(a);
       with_bwd_cfg(a.d, [&](auto c, int) {
         using C = decltype(c);
-        norm_bwd_kernel<Y, R, X, C::LPR, C::CH, C::SHORT><<<dim3(parts), threads_of(C::LPR), 0, s>>>(a);
+        norm_bwd_kernel<Y, R, X, C::LPR, C::CH, C::SHORT><<<dim3(parts + a.dw_blocks), threads_of(C::LPR), 0, s>>>(a);
       });
     });
-  if (a.dw) norm_dw_kernel<<<dim3((a.d + DW_COLS - 1) / DW_COLS), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
+  if (a.dw && !a.dw_blocks) norm_dw_kernel<<<dim3(dw_blocks), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
   return hipGetLastError();
 }
 

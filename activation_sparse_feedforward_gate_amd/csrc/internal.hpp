@@ -262,11 +262,12 @@ struct NormArgs {
   float keep_scale;          // 1 / (1 - drop / 65536), 0 where everything is dropped
   float eps;
   float* dw;
-  float* part;               // [norm_bwd_parts(T, d)][d] row sums of dw
+  float* part;               // [norm_bwd_parts(T, d)][d] row sums of dw, or null
+  int dw_blocks;             // workgroups that compute dw without them
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 int norm_bwd_parts(int T, int d);
-hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(NormArgs a, hipStream_t s);
 hipError_t launch_dropout_add(const NormArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights (block_w4.hip)

@@ -406,3 +406,40 @@ def test_norm_on_another_stream_and_in_a_graph(torch, tw):
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, got)), k
+
+
+@pytest.mark.parametrize("T,d", [(1024, 40), (1025, 40), (1024, 4096), (1024, 4104), (1025, 5000), (1024, 8), (65, 1003)])
+def test_norm_bwd_both_ways_to_dw(torch, tw, T, d):
+    """Sizes on both sides of the rule that takes dw from workgroups of its own."""
+    bwd_case(torch, tw, T, d, "f32", "bf16", "bf16", 0.1)
+    bwd_case(torch, tw, T, d, "bf16", "f32", "f32", 0.0)
+
+
+@pytest.mark.parametrize("T,d", [(70, 1003), (1100, 45)])
+def test_norm_bwd_strided_and_in_place(torch, tw, T, d):
+    """Rows inside wider buffers and dres written over dsum: the same bits as
+    from rows side by side."""
+    r = np.random.default_rng(11)
+    sh = tw.norm_shape(T, d, 1, 1, 0, 1, EPS, 0.25)
+    dy, ds, s = (make(torch, r, T, d, t) for t in (torch.float32, torch.bfloat16, torch.bfloat16))
+    w, rstd, rng = make(torch, r, 1, d, torch.bfloat16), torch.rand(T, device="cuda") + 0.5, rng_tensor(torch)
+    ws = torch.empty(tw.twell_add_rmsnorm_bwd_workspace(sh), dtype=torch.uint8, device="cuda")
+
+    def wide(t, at, more):
+        b = torch.full((T, d + more), 7.0, dtype=t.dtype, device="cuda")
+        b[:, at:at + d] = t
+        return b, b[:, at:at + d]
+
+    got = []
+    for strided in (False, True):
+        log(f"[norm bwd strided] T={T} d={d} strided={strided}")
+        (yb, y), (db, dres), (sb, sv), (xb, dx) = ((t, t) if not strided else wide(t, at, more) for t, at, more in (
+            (dy, 3, 8), (ds.clone(), 1, 3), (s, 5, 6), (torch.zeros_like(ds), 2, 9)))
+        dw = torch.empty(d, device="cuda")
+        tw.twell_add_rmsnorm_bwd(sh, y, dres, sv, w, rstd, rng, dres, dx, dw, ws)
+        got.append((dres.clone(), dx.clone(), dw))
+        if strided:
+            assert (db[:, :1] == 7).all() and (db[:, 1 + d:] == 7).all()
+            assert (xb[:, :2] == 7).all() and (xb[:, 2 + d:] == 7).all()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
