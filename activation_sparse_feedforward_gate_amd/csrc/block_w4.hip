@@ -66,16 +66,15 @@ __device__ __forceinline__ bf16x8 w_bf16(uint32_t codes, float scale) {
   const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
   return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
-// acc[I ..] += v times eight codes of weights, times scale.
-template <int I>
-__device__ __forceinline__ void add8(uint32_t codes, float scale, float v, float acc[32]) {
+// acc += v times eight codes of weights, times scale.
+__device__ __forceinline__ void add8(uint32_t codes, float scale, float v, float acc[8]) {
   const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 0);
   const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 1);
   const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 2);
   const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 3);
   const float w[8] = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[I + i] += v * w[i];
+  for (int i = 0; i < 8; ++i) acc[i] += v * w[i];
 }
 // Eight codes of tokens as bf16, times scale.
 __device__ __forceinline__ u32x4 x_bf16(uint32_t lo, uint32_t hi, float scale) {
@@ -582,38 +581,50 @@ __global__ __launch_bounds__(64 * GEMV_WAVES) void w4_gate_up_gemv_kernel(W4Args
 
 // ---------------------------------------------------------------- the down product
 
-// y_t = sum over the pairs (t, n) that fire, n ascending within a slot, of
-// a * Wd[n].  One workgroup per token and DB blocks of 32 columns: the pairs are
-// listed in LDS from their bits, NS slots take every NS-th pair, a thread one
-// slot and one block (16 bytes of codes, one scale), and the slots are added in
-// order.
-constexpr int DB = 8, NS = 32, DU = 4, DLIST = 2048;
+// y_t = sum over the pairs (t, n) that fire of a * Wd[n].  One workgroup per token
+// and DC columns: the pairs are listed in LDS from their bits, in order; DL lanes take
+// a row, eight columns each (whole lines), DS slots every DS-th pair with DU of them in
+// flight, and the slots are added in order.  Its time is a chain of waits: bits, list,
+// rows, sums.
+constexpr int DLIST = 2048;
+template <int DC_, int DS_, int DU_>
+struct Down {
+  static constexpr int DC = DC_, DL = DC / 8, DS = DS_, DU = DU_, DTH = DL * DS;
+};
 
-__global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);        // from 1, 2, 4, 8 lanes down in 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);       // lane 15 of the 16 before, to every other 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);       // lane 31, to the upper half
+  return v;
+}
+
+template <class C>
+__global__ __launch_bounds__(C::DTH) void w4_down_kernel(W4Args a) {
+  constexpr int DC = C::DC, DL = C::DL, DS = C::DS, DU = C::DU, DTH = C::DTH;
   __shared__ int ln[DLIST];
-  __shared__ float part[NS][DB][33];
-  __shared__ int wsum[DB * NS / 64];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int slot = tid / DB, b = blockIdx.x * DB + tid % DB, nblk = a.K / 32;
-  const bool live = b < nblk;
+  __shared__ __attribute__((aligned(16))) float part[DS][DC];
+  __shared__ int wsum[DTH / 64];
+  const int tid = threadIdx.x, w = tid >> 6;
+  const int slot = tid / DL, c = blockIdx.x * DC + tid % DL * 8, nblk = a.K / 32;
+  const bool live = c < a.K;
   for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
     const uint64_t* mask = (const uint64_t*)(a.mask + t * (a.N / 16));
     const float* act = a.act + t * a.N;
-    float acc[32] = {};
-    for (int w0 = 0; w0 < a.N / 64; w0 += DB * NS) {
+    float acc[8] = {};
+    for (int w0 = 0; w0 < a.N / 64; w0 += DTH) {
       uint64_t m = w0 + tid < a.N / 64 ? mask[w0 + tid] : 0;
       const int cnt = popc64(m);
-      int pre = cnt;                                    // inclusive scan over the workgroup
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(pre, o);
-        if (lane >= o) pre += v;
-      }
-      if (lane == 63) wsum[w] = pre;
+      int pre = wave_scan(cnt);
+      if ((tid & 63) == 63) wsum[w] = pre;
       __syncthreads();
       int total = 0;
 #pragma unroll
-      for (int i = 0; i < DB * NS / 64; ++i) {
+      for (int i = 0; i < DTH / 64; ++i) {
         if (i < w) pre += wsum[i];
         total += wsum[i];
       }
@@ -628,38 +639,34 @@ __global__ __launch_bounds__(DB * NS) void w4_down_kernel(W4Args a) {
         __syncthreads();
         const int cntr = min(DLIST, total - e0);
         if (live)
-          for (int i0 = slot; i0 < cntr; i0 += NS * DU) {
-            u32x4 q[DU];
-            float v[DU], sc[DU];
+          for (int i0 = slot; i0 < cntr; i0 += DS * DU) {
+            uint32_t q[DU], sc[DU];
+            float v[DU];
 #pragma unroll
             for (int u = 0; u < DU; ++u) {
-              const int64_t n = ln[min(i0 + u * NS, cntr - 1)];
+              const int64_t n = ln[min(i0 + u * DS, cntr - 1)];
               v[u] = act[n];
-              q[u] = *(const u32x4*)(a.Wd.code + n * (a.K / 2) + b * 16);
-              sc[u] = __uint_as_float((uint32_t)a.Wd.scale[n * nblk + b] << 23);
+              q[u] = *(const uint32_t*)(a.Wd.code + n * (a.K / 2) + c / 2);
+              sc[u] = a.Wd.scale[n * nblk + c / 32];
             }
 #pragma unroll
             for (int u = 0; u < DU; ++u)
-              if (i0 + u * NS < cntr) {
-                add8<0>(q[u].x, sc[u], v[u], acc);
-                add8<8>(q[u].y, sc[u], v[u], acc);
-                add8<16>(q[u].z, sc[u], v[u], acc);
-                add8<24>(q[u].w, sc[u], v[u], acc);
-              }
+              if (i0 + u * DS < cntr) add8(q[u], scale_of(sc[u]), v[u], acc);
           }
         __syncthreads();
       }
       __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) part[slot][tid % DB][i] = acc[i];
+    *(f32x4*)&part[slot][tid % DL * 8] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+    *(f32x4*)&part[slot][tid % DL * 8 + 4] = f32x4{acc[4], acc[5], acc[6], acc[7]};
     __syncthreads();
-    const int c = blockIdx.x * (DB * 32) + tid;
-    if (c < a.K) {
-      float s = part[0][tid / 32][tid % 32];
-      for (int i = 1; i < NS; ++i) s += part[i][tid / 32][tid % 32];
-      if (a.y_bf16) ((uint16_t*)a.y)[t * a.ldy + c] = (uint16_t)bf16_round(s);
-      else ((float*)a.y)[t * a.ldy + c] = s;
+    const int o = blockIdx.x * DC + tid;
+    if (tid < DC && o < a.K) {            // DC <= DTH
+      float s = part[0][tid];
+#pragma unroll
+      for (int i = 1; i < DS; ++i) s += part[i][tid];
+      if (a.y_bf16) ((uint16_t*)a.y)[t * a.ldy + o] = (uint16_t)bf16_round(s);
+      else ((float*)a.y)[t * a.ldy + o] = s;
     }
     __syncthreads();
   }
@@ -721,6 +728,16 @@ int tile_waves(const W4Args& a) {
   return waves < most ? waves : most;
 }
 
+// Calls f with the down product's workgroup: 64 columns and many slots, the shortest
+// chain, while there are few of them; 256 columns list the pairs a quarter as often.
+// The layer, one token at 2304 x 9216: 9.7 us and 10.3; 48 tokens at 4096 x 6144: 30.3
+// and 24.8.
+template <class F>
+void with_down(const W4Args& a, F f) {
+  if ((int64_t)a.T * ((a.K + 63) / 64) <= 512) f(Down<64, 32, 4>{});
+  else f(Down<256, 16, 6>{});
+}
+
 bool use_gemv(const W4Args& a) { return a.T <= GEMV_T; }
 
 // Calls f with the tokens of the kernel and its workgroup.
@@ -765,7 +782,10 @@ hipError_t launch_ffn_w4(W4Args a, void* ws, hipStream_t s) {
       w4_gate_up_kernel<C><<<tile_grid<C>(a), 64 * tile_waves<C>(a), tile_lds<C>(tile_waves<C>(a)), s>>>(a);
     });
   }
-  w4_down_kernel<<<dim3((a.K + DB * 32 - 1) / (DB * 32), a.T < TOKEN_GRID ? a.T : TOKEN_GRID), DB * NS, 0, s>>>(a);
+  with_down(a, [&](auto c) {
+    using C = decltype(c);
+    w4_down_kernel<C><<<dim3((a.K + C::DC - 1) / C::DC, a.T < TOKEN_GRID ? a.T : TOKEN_GRID), C::DTH, 0, s>>>(a);
+  });
   return hipGetLastError();
 }
 
