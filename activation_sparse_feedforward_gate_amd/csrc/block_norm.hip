@@ -466,13 +466,14 @@ struct Cfg {
 // Few chunks per lane and few idle lanes: two or three chunks in flight per lane
 // fill the memory pipe, more cost registers and so waves.  32768 rows of 2304
 // (fp32 x, bf16 rest, dropout): <128, 3> 129 us (5.8 TB/s), <256, 2> 144, <64, 5>
-// 166, <64, 8> 273.  Up to 512 rows the time is one row's latency and one chunk
-// a lane is fastest: 1 row of 2304 to MXFP8, <512, 1> 3.5 us, <256, 2> 4.2, <128, 3>
-// 5.2; 1024 rows, 7.7, 6.5 and 6.9.
+// 166, <64, 8> 273.  Up to 1024 rows the time is one row's latency and one chunk a
+// lane is fastest: 1 row of 2304 to MXFP8, <512, 1> 3.3 us, <256, 2> 4.2, <128, 3> 5.2;
+// 700 rows of 2048, <256, 1> 4.7, <128, 2> 5.5; 1024 of 2304, 8.0 and 8.0; 1500 of
+// 4096, 12.5 and 12.3.
 template <class F>
 void with_fwd_cfg(int T, int d, F f) {
   if (d < 8) return f(Cfg<16, 1, true>{});
-  if (T <= 512 && d > 512) {
+  if (T <= 1024 && d > 512) {
     if (d <= 2048) return f(Cfg<256, 1>{});
     if (d <= 4096) return f(Cfg<512, 1>{});
   }
@@ -492,8 +493,7 @@ void with_fwd_cfg(int T, int d, F f) {
 // The backward holds two inputs, the gradient and its part of dw per chunk, and
 // its workgroups (the second argument: as many as 256 CUs hold at once) walk
 // the rows, so that a part of dw is written once.  32768 rows of 2304: <512, 1>
-// 183 us (4.9 TB/s), <128, 3> 183, <256, 2> 189, <64, 5> 248; with twice the
-// workgroups 188, 187, 196, 252.
+// 181 us (5.0 TB/s; 187 with twice the workgroups), <128, 3> 226, <256, 2> 288.
 constexpr int BWD_MAX_D = 16384;
 template <class F>
 void with_bwd_cfg(int d, F f) {
