@@ -98,7 +98,12 @@ struct Tile {
   static constexpr int XP = XB + 16;                 // and of its row in LDS: 16 tokens' same unit lies in all banks
   static constexpr int XL = XB * 16 / 1024;          // loads of a chunk of 16 tokens
 };
-constexpr int WP = 80;                               // the same of 64 bytes of a row's codes
+constexpr int WP = 64;                               // bytes of a row's codes there
+// Where 16 bytes `unit` of a row's codes lie: neighbouring lanes write four units of a
+// row, and read one unit of as many rows, from all banks either way.
+__device__ __forceinline__ int w_at(int row, int unit) {
+  return row * WP + (unit ^ ((row >> 1) & 3) ^ (row >> 3 & 1)) * 16;
+}
 // A wave's piece of LDS.
 template <class C>
 struct WaveLds {
@@ -170,9 +175,9 @@ __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, R
     xsp[t] = MX ? a.x_scale + (int64_t)min(t0 + 16 * t + lane / 4, a.T - 1) * blocks : nullptr;
   }
   char* const xw = my.x + xt * C::XP + xu;
-  char* const ww = my.w + (lane / 4) * WP + (lane & 3) * 16;
+  char* const ww = my.w + w_at(lane / 4, lane & 3);
   const char* const xr = my.x + lo * C::XP + hi * (C::XB / 4);   // block hi of token lo
-  const char* const wr = my.w + lo * WP + hi * 16;               // block hi of row lo
+  const char* const wr = my.w + w_at(lo, hi);                    // block hi of row lo
 
   f32x4 acc[RT][TT];
 #pragma unroll
