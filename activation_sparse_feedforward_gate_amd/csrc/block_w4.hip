@@ -18,8 +18,8 @@
 // A vector instruction of a wave takes a SIMD 1.8 ns (the conversions are no slower
 // than others), so a few hundred of them are as long as the memory's part of a small
 // call: the loops below hold little beside the conversions.
-// 16 tokens, 40001 x 2048 (46 MB): 12.4 us, 3.7 TB/s; 30001 x 4096 (66 MB): 14.9 us,
-// 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.7 us, of which a launch is about four.
+// 16 tokens, 40001 x 2048 (46 MB): 11.4 us, 4.1 TB/s; 30001 x 4096 (66 MB): 14.5 us,
+// 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.6 us, of which a launch is about four.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -87,13 +87,14 @@ __device__ __forceinline__ u32x4 x_bf16(uint32_t lo, uint32_t hi, float scale) {
 // ---------------------------------------------------------------- the matrix path
 
 // The waves of a workgroup split K; each has RT tiles of 16 rows times TT tiles of
-// 16 tokens.  Up to WAVES waves, with the registers of OCC a SIMD.
-template <bool MX_, int RT_, int TT_, int WAVES_, int OCC_>
+// 16 tokens, with the loads of D chunks in flight.  Up to WAVES waves, with the
+// registers of OCC a SIMD.
+template <bool MX_, int RT_, int TT_, int WAVES_, int OCC_, int D_>
 struct Tile {
   static constexpr bool MX = MX_;
   static constexpr int RT = RT_, TT = TT_, ROWS = 16 * RT, TOKS = 16 * TT;
   static constexpr int E = RT * TT;                  // 16x16 results
-  static constexpr int WAVES = WAVES_, OCC = OCC_;
+  static constexpr int WAVES = WAVES_, OCC = OCC_, D = D_;
   static constexpr int XB = MX ? 128 : 256;          // bytes of a token's chunk
   static constexpr int XP = XB + 16;                 // and of its row in LDS: 16 tokens' same unit lies in all banks
   static constexpr int XL = XB * 16 / 1024;          // loads of a chunk of 16 tokens
@@ -148,7 +149,7 @@ __device__ __forceinline__ uint32_t scales_at(uint32_t v, int b, int blocks) {
 // Each wave takes a run of K's chunks, in pieces of four (their scales are one load).
 template <class C, class Row, class Out>
 __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, Row row, int t0, char* lds, Out out) {
-  constexpr int RT = C::RT, TT = C::TT, XL = C::XL;
+  constexpr int RT = C::RT, TT = C::TT, XL = C::XL, D = C::D;
   constexpr bool MX = C::MX;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int lo = lane & 15, hi = lane >> 4;
@@ -236,16 +237,19 @@ __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, R
   };
 
   if (c0 < c1) {
-    u32x4 wf[RT], xf[TT][XL];                        // one chunk in flight: with more the registers do not last
+    u32x4 wf[D][RT], xf[D][TT][XL];
     uint32_t sf[RT], xsf[TT] = {};
-    auto load = [&](int ck) {                        // blocks past the row's end: its last one, not used
+    // Chunks past the wave's end: its last one again, and blocks past the row's end:
+    // its last one, neither used.
+    auto load = [&](int ck, int slot) {
+      ck = min(ck, c1 - 1);
       const int wo = min(ck * 64 + (lane & 3) * 16, blocks * 16 - 16), xo = min(ck * C::XB + xu, blocks * (C::XB / 4) - 16);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) wf[r] = *(const u32x4*)(wp[r] + wo);
+      for (int r = 0; r < RT; ++r) wf[slot][r] = *(const u32x4*)(wp[r] + wo);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < XL; ++i) xf[t][i] = load16(xp[t][i] + xo);
+        for (int i = 0; i < XL; ++i) xf[slot][t][i] = load16(xp[t][i] + xo);
     };
     auto load_piece_scales = [&](int ck) {
 #pragma unroll
@@ -256,39 +260,51 @@ __device__ __forceinline__ void tile_product(const W4Args& a, const W4View& W, R
       }
     };
     load_piece_scales(c0);
-    load(c0);
-    // Not unrolled: a short call runs this code once or twice, and instructions that
-    // are not in the cache yet cost more than the loop's few.
-#pragma unroll 1
-    for (int ck = c0; ck < c1; ++ck) {
-      const int p = (ck - c0) & 3;
-      if (p == 0) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) my.s[r][lane] = scales_at(sf[r], (ck + (lane & 3)) * 4, blocks);
-        if constexpr (MX) {
+    for (int c = 0; c < D; ++c) load(c0 + c, c);
+    auto piece = [&](int g, auto last) {
 #pragma unroll
-          for (int t = 0; t < TT; ++t) my.xs[t][lane] = scales_at(xsf[t], (ck + (lane & 3)) * 4, blocks);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) *(u32x4*)(ww + 16 * r * WP) = wf[r];
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = xf[t][i];
-      wave_lds_fence();
-      if (ck + 1 < c1) load(ck + 1);
-      if (p == 0 && ck + 4 < c1) load_piece_scales(ck + 4);
-      uint32_t s[RT], xs[TT] = {};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) s[r] = my.s[r][4 * lo + p];
+      for (int r = 0; r < RT; ++r) my.s[r][lane] = scales_at(sf[r], (g + (lane & 3)) * 4, blocks);
       if constexpr (MX) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) xs[t] = my.xs[t][4 * lo + p];
+        for (int t = 0; t < TT; ++t) my.xs[t][lane] = scales_at(xsf[t], (g + (lane & 3)) * 4, blocks);
       }
-      multiply(s, xs, blocks - 4 * ck);
-      wave_lds_fence();
-    }
+      if constexpr (!last.value) load_piece_scales(g + 4);
+      u32x4 sc[RT], xsc[TT];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (last.value && g + c >= c1) break;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) *(u32x4*)(ww + 16 * r * WP) = wf[c % D][r];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int i = 0; i < XL; ++i) *(u32x4*)(xw + (16 * t + i * TPL) * C::XP) = xf[c % D][t][i];
+        wave_lds_fence();
+        if (c == 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) sc[r] = *(const u32x4*)&my.s[r][4 * lo];
+          if constexpr (MX) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) xsc[t] = *(const u32x4*)&my.xs[t][4 * lo];
+          }
+        }
+        if (!last.value || c + D < 4) load(g + c + D, c % D);
+        uint32_t s[RT], xs[TT] = {};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = sc[r][c];
+        if constexpr (MX) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) xs[t] = xsc[t][c];
+        }
+        multiply(s, xs, blocks - 4 * (g + c));
+        wave_lds_fence();
+      }
+    };
+    int g = c0;
+#pragma unroll 1
+    for (; g + 4 < c1; g += 4) piece(g, std::false_type{});
+    piece(g, std::true_type{});
   }
   __syncthreads();                                   // the sums lie over the waves' pieces
   f32x4 (*sum)[C::E][64] = (f32x4(*)[C::E][64])lds;
@@ -360,7 +376,7 @@ __global__ __launch_bounds__(64 * C::WAVES, C::OCC) void w4_matvec_kernel(W4Args
 // workgroup's rows.
 template <class C>
 __global__ __launch_bounds__(64 * C::WAVES, C::OCC) void w4_gate_up_kernel(W4Args a) {
-  using U = Tile<C::MX, 1, C::TT, C::WAVES, C::OCC>;
+  using U = Tile<C::MX, 1, C::TT, C::WAVES, C::OCC, C::D>;
   __shared__ uint32_t fires[C::RT];                  // of each tile of 16 rows
   __shared__ float hl[C::TOKS][C::ROWS + 1];         // max(g, 0), NaN as 0
   __shared__ int list[C::ROWS];                      // the rows that fire
@@ -684,13 +700,16 @@ namespace {
 // grows with both), which read the tokens half as often, or there is no more than
 // one of 16 x 16 for each CU.  With the other tile: 64 tokens, 40001 x 2048, 26 us and
 // 42 (small); 9216 x 2304, 11.5 and 13 (large) and 20.8 (narrow); 30 tokens, 700 x
-// 8192, 6.2 and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0 (narrow).
+// 8192, 6.2 and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0 (narrow).  MXFP8
+// tokens take half the registers and leave room for a second chunk in flight (16
+// tokens, 40001 x 2048: 12.4 us, and 11.4 with it; in bf16, 64 tokens, 9216 x 2304, 11.1
+// and 11.8).
 template <bool MX>
-using Narrow = Tile<MX, 1, 1, 8, 4>;
+using Narrow = Tile<MX, 1, 1, 8, 3, MX ? 2 : 1>;
 template <bool MX>
-using Small = Tile<MX, 2, 1, 8, 3>;
+using Small = Tile<MX, 2, 1, 8, 3, MX ? 2 : 1>;
 template <bool MX>
-using Large = Tile<MX, 4, 2, 4, 2>;
+using Large = Tile<MX, 4, 2, 4, 2, 1>;
 template <bool PRODUCT, class F>
 void with_tile(const W4Args& a, F f) {
   auto go = [&](auto mx) {
