@@ -198,13 +198,18 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_fwd_kernel(NormArgs a) {
   }
 }
 
-// Rows of 32 columns of dw by a workgroup of its own, from dy, sum and rstd alone:
-// 8 columns a thread, its rows added in order and the threads' sums after them.
+// Some columns of dw by a workgroup of its own, from dy, sum and rstd alone: 8 columns
+// a thread, its rows added in order and the threads' sums after them.  As few columns
+// as whole 64-byte pieces of both rows allow where a workgroup has only four waves for
+// the rows (777 rows of 1001 fp32: 8.8 us, 9.6 with 32 columns).
 constexpr int DW_COLS = 32;
+constexpr int dw_cols(int y_size, int r_size, int threads) {
+  return y_size == 4 && r_size == 4 && threads == 256 ? 16 : DW_COLS;
+}
 template <class Y, class R, int NTH>
-__device__ __forceinline__ void dw_columns(const NormArgs& a, int c0, float* sh) {
-  constexpr int TPR = DW_COLS / 8, ROWS = NTH / TPR, U = 4;
-  const int y = threadIdx.x / TPR, c = c0 + threadIdx.x % TPR * 8, cl = min(c, (a.d - 1) / 8 * 8);
+__device__ __forceinline__ void dw_columns(const NormArgs& a, int block, float* sh) {
+  constexpr int COLS = dw_cols(Y::size, R::size, NTH), TPR = COLS / 8, ROWS = NTH / TPR, U = 4;
+  const int c0 = block * COLS, y = threadIdx.x / TPR, c = c0 + threadIdx.x % TPR * 8, cl = min(c, (a.d - 1) / 8 * 8);
   float s[8] = {};
   for (int64_t t0 = y; t0 < a.T; t0 += ROWS * U) {
     Raw8<Y> yv[U];
@@ -232,12 +237,12 @@ __device__ __forceinline__ void dw_columns(const NormArgs& a, int c0, float* sh)
   for (int i = 0; i < 8; ++i) {
 #pragma unroll
     for (int o = TPR; o < 64; o <<= 1) s[i] += __shfl_xor(s[i], o);
-    if ((threadIdx.x & 63) < TPR) sh[threadIdx.x / 64 * DW_COLS + threadIdx.x % TPR * 8 + i] = s[i];
+    if ((threadIdx.x & 63) < TPR) sh[threadIdx.x / 64 * COLS + threadIdx.x % TPR * 8 + i] = s[i];
   }
   __syncthreads();
-  if (threadIdx.x < DW_COLS && c0 + (int)threadIdx.x < a.d) {
+  if (threadIdx.x < COLS && c0 + (int)threadIdx.x < a.d) {
     float v = sh[threadIdx.x];
-    for (int w = 1; w < NTH / 64; ++w) v += sh[w * DW_COLS + threadIdx.x];
+    for (int w = 1; w < NTH / 64; ++w) v += sh[w * COLS + threadIdx.x];
     a.dw[c0 + threadIdx.x] = v;
   }
 }
@@ -251,7 +256,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int ROW_SH = RPB > 1 ? 8 * NTH : NTH / 64, COL_SH = NTH / 64 * DW_COLS;
   __shared__ float sh[ROW_SH > COL_SH ? ROW_SH : COL_SH];
   if constexpr (!SHORT)
-    if ((int)blockIdx.x < a.dw_blocks) return dw_columns<Y, R, NTH>(a, blockIdx.x * DW_COLS, sh);
+    if ((int)blockIdx.x < a.dw_blocks) return dw_columns<Y, R, NTH>(a, blockIdx.x, sh);
   const int block = blockIdx.x - a.dw_blocks, blocks = gridDim.x - a.dw_blocks;
   const int lane = threadIdx.x % LPR;
   Philox g{};
@@ -526,7 +531,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
 
 // Whether dw comes from workgroups of its own: they read dy and sum again, and save the
 // second launch (about 3 us) and the parts.  Rows 1 of 2304: 3.7 us, 7.2 by parts; 500
-// of 4096: 8.7 and 12.4; 777 of 1001 fp32: 9.6 and 10.3; 1024 of 2304: 11.6 and 12.5;
+// of 4096: 8.7 and 12.4; 777 of 1001 fp32: 8.8 and 10.3; 1024 of 2304: 11.6 and 12.5;
 // 1000 of 8000: 26.6 and 22.4; 2000 of 512: 11.1 and 9.1.
 bool dw_apart(const NormArgs& a) {
   return a.d >= 8 && a.d <= BWD_MAX_D && a.T <= 1024 && (int64_t)a.T * a.d <= 4 << 20;
@@ -543,22 +548,22 @@ int norm_bwd_parts(int T, int d) {
 }
 
 hipError_t launch_norm_bwd(NormArgs a, hipStream_t s) {
-  const int parts = norm_bwd_parts(a.T, a.d), dw_blocks = (a.d + DW_COLS - 1) / DW_COLS;
-  if (!a.dw) a.part = nullptr;
-  if (a.dw && a.T > 0 && dw_apart(a)) {
-    a.dw_blocks = dw_blocks;
-    a.part = nullptr;
-  }
+  const int parts = norm_bwd_parts(a.T, a.d);
+  const bool apart = a.dw && a.T > 0 && dw_apart(a);
+  if (!a.dw || apart) a.part = nullptr;
   if (a.T > 0)
     with_types(a.y.dt, a.res.dt, a.x.dt, [&](auto y, auto r, auto x) {
       using Y = decltype(y); using R = decltype(r); using X = decltype(x);
       if (a.d > BWD_MAX_D) return norm_bwd_wide_kernel<Y, R, X><<<dim3(parts), WIDE, 0, s>>>(a);
       with_bwd_cfg(a.d, [&](auto c, int) {
         using C = decltype(c);
+        const int cols = dw_cols(Y::size, R::size, threads_of(C::LPR));
+        a.dw_blocks = apart ? (a.d + cols - 1) / cols : 0;
         norm_bwd_kernel<Y, R, X, C::LPR, C::CH, C::SHORT><<<dim3(parts + a.dw_blocks), threads_of(C::LPR), 0, s>>>(a);
       });
     });
-  if (a.dw && !a.dw_blocks) norm_dw_kernel<<<dim3(dw_blocks), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
+  if (a.dw && !apart)
+    norm_dw_kernel<<<dim3((a.d + DW_COLS - 1) / DW_COLS), DW_COLS * DW_ROWS, 0, s>>>(a.part, parts, a.d, a.dw);
   return hipGetLastError();
 }
 

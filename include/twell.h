@@ -608,7 +608,8 @@ typedef struct {
 
 /*
  * twell_w4_matvec: y = x . W^T + bias for a few tokens, accumulated in fp32;
- * any T >= 0 and N >= 1.  The weights are read once per 64 tokens.
+ * any T >= 0 and N >= 1.  Made for up to 64 tokens: the weights are read again
+ * for every 16 of them (32 of a wide product).
  *   x        [T][K], rows ldx elements apart, x_dt BF16, or MXFP8 with
  *            x_scale [T][K / 32] (NULL for BF16): what twell_add_rmsnorm_fwd
  *            writes
@@ -625,9 +626,8 @@ size_t twell_ffn_fwd_w4_workspace(const twell_ffn_shape *sh);
 
 /*
  * twell_ffn_fwd_w4: the layer of twell_ffn_fwd on MXFP4 weights Wg, Wu and Wd
- * (each N = F, K = d), for the few tokens of a serving step: the gate reads Wg
- * once per 64 tokens, and of Wu and Wd only the rows of neurons that fire
- * (g > 0 in fp32) are read.  in_dt BF16 or MXFP8 (of x), out_dt F32 or BF16;
+ * (each N = F, K = d), for the few tokens of a serving step: of Wu and Wd only
+ * the rows of neurons that fire (g > 0 in fp32) are read.  in_dt BF16 or MXFP8 (of x), out_dt F32 or BF16;
  * products and h, u, a are accumulated and kept in fp32.
  *   x        [T][d]; x_scale [T][d / 32] for MXFP8, NULL for BF16
  *   bg       [F] BF16 or NULL

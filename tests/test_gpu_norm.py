@@ -443,3 +443,8 @@ def test_norm_bwd_strided_and_in_place(torch, tw, T, d):
             assert (xb[:, :2] == 7).all() and (xb[:, 2 + d:] == 7).all()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,d", [(1024, 9), (130, 1009), (1000, 2041), (300, 2500)])
+def test_norm_bwd_fp32_columns_of_dw(torch, tw, T, d):
+    bwd_case(torch, tw, T, d, "f32", "f32", "f32", 0.1)
