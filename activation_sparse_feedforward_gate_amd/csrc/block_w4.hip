@@ -695,26 +695,31 @@ __global__ __launch_bounds__(C::DTH) void w4_down_kernel(W4Args a) {
 
 namespace {
 
-// Calls f with the tile for the tokens and rows: 32 rows x 16 tokens, unless there
-// are enough workgroups of 64 x 32 (of a product; the layer's list of rows that fire
-// grows with both), which read the tokens half as often, or there is no more than
-// one of 16 x 16 for each CU.  With the other tile: 64 tokens, 40001 x 2048, 26 us and
-// 42 (small); 9216 x 2304, 11.5 and 13 (large) and 20.8 (narrow); 30 tokens, 700 x
-// 8192, 6.2 and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0 (narrow).  MXFP8
-// tokens take half the registers and leave room for a second chunk in flight (16
-// tokens, 40001 x 2048: 12.4 us, and 11.4 with it; in bf16, 64 tokens, 9216 x 2304, 11.1
-// and 11.8).
+// Calls f with the tile for the tokens and rows.  32 rows x 16 tokens, unless there is
+// no more than one workgroup of 16 x 16 for each CU, or more than 16 tokens go with
+// enough rows of a product for tiles that read them half as often (the layer's list of
+// rows that fire grows with its tile).  With the tile of the neighbouring range: 30
+// tokens, 700 x 8192, 6.2 us and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0
+// (narrow); 9216 x 2304, 11.4 and 11.8 (middle); 12000 x 2048, 11.9 and 14.3 (small);
+// 20 tokens, 16000 x 4096, 12.0 and 16.8 (small); 64 tokens, 40001 x 2048, 25 and 28
+// (middle).  MXFP8 tokens take half the registers and leave room for a second chunk in
+// flight (16 tokens, 40001 x 2048: 12.4 us, and 11.4 with it; in bf16, 64 tokens, 9216
+// x 2304, 11.1 and 11.8).
 template <bool MX>
 using Narrow = Tile<MX, 1, 1, 8, 3, MX ? 2 : 1>;
 template <bool MX>
 using Small = Tile<MX, 2, 1, 8, 3, MX ? 2 : 1>;
 template <bool MX>
+using Middle = Tile<MX, 2, 2, 4, 2, 1>;
+template <bool MX>
 using Large = Tile<MX, 4, 2, 4, 2, 1>;
 template <bool PRODUCT, class F>
 void with_tile(const W4Args& a, F f) {
   auto go = [&](auto mx) {
-    if constexpr (PRODUCT)
+    if constexpr (PRODUCT) {
       if (a.T > 16 && a.N > 16384) return f(Large<mx.value>{});
+      if (a.T > 16 && a.N > 10240) return f(Middle<mx.value>{});
+    }
     if ((int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16) <= 256) f(Narrow<mx.value>{});
     else f(Small<mx.value>{});
   };

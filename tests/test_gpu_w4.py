@@ -358,3 +358,9 @@ def test_matvec_splits(torch, tw, T, N, K, kind):
     y = out(torch, T, N, "f32")
     tw.twell_w4_matvec(x, xs, W, None, y)
     check_product(values(y), xv, w, None, "f32")
+
+
+@pytest.mark.parametrize("T,N,K", [(17, 10241, 416), (64, 10300, 1184), (33, 16384, 96), (17, 10240, 416), (70, 12001, 512)])
+@pytest.mark.parametrize("kind", ["bf16", "mx8"])
+def test_matvec_middle_sizes(torch, tw, T, N, K, kind):
+    test_matvec_splits(torch, tw, T, N, K, kind)
