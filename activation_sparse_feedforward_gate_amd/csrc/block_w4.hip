@@ -741,20 +741,22 @@ dim3 tile_grid(const W4Args& a) {
   return dim3((a.N + C::ROWS - 1) / C::ROWS, toks < TOKEN_GRID ? toks : TOKEN_GRID);
 }
 
-// The same of the matrix path: one per four chunks where workgroups are many (the
-// waves' sums go through LDS at the end), otherwise one per chunk; up to four, and to
-// eight where there is no more than a workgroup for each CU and K is long.  9 tokens,
-// 3001 x 480: 3.2 us, and 4.0 with one per four; 64 tokens, 65536 x 512: 19.9 and 15.7;
-// 5 tokens, 5000 x 16384: 13.2, and 17.1 with four; 64 tokens, 9216 x 2304: 14.6 and
-// 11.5.
+// The same of the matrix path.  Where workgroups are many, about one per four chunks (the
+// waves' sums go through LDS at the end) and no three, which load the SIMDs unevenly;
+// otherwise one per chunk, up to four, and to eight where there is no more than a
+// workgroup for each CU and K is long.  9 tokens, 3001 x 480: 3.2 us, and 4.0 with one
+// per four; 5 tokens, 5000 x 16384: 13.2, and 17.1 with four; 64 tokens, 9216 x 2304:
+// 14.6 with eight and 11.5; 41 tokens, 39755 x 1248: 22.7 with four, 25.4 with three; 64
+// tokens, 16000 x 1024: 8.0 with two, 10.4 with three; 65536 x 512: 18.7 with two, 15.2
+// with one.
 template <class C>
 int tile_waves(const W4Args& a) {
   const dim3 g = tile_grid<C>(a);
   const int64_t groups = (int64_t)g.x * g.y;
   const int chunks = (a.K + CHUNK - 1) / CHUNK;
-  const int waves = C::TT > 1 || groups > 1024 ? (chunks + 3) / 4 : chunks;
-  const int most = C::WAVES > 4 && groups <= 256 && (C::RT == 1 || chunks >= 32) ? 8 : 4;
-  return waves < most ? waves : most;
+  if (C::TT > 1 || groups > 1024) return chunks > 8 ? 4 : chunks > 4 ? 2 : 1;
+  const int most = groups <= 256 && (C::RT == 1 || chunks >= 32) ? 8 : 4;
+  return chunks < most ? chunks : most;
 }
 
 // Calls f with the down product's workgroup: 64 columns and many slots, the shortest
