@@ -56,30 +56,30 @@ def _ffn(name, T, d, F, x, y, density):
 def listed():
     return [
         # one decoded token ahead of the 2b-sized layer: pure latency
-        _norm("norm one token to 8 bits", 1, 2304, "f32", "bf16", "mx8", 0.0),
+        _norm("norm, one token, to 8 bits", 1, 2304, "f32", "bf16", "mx8", 0.0),
         # a ragged prompt chunk of the 1.5b-sized layer, written as 8 bits
-        _norm("norm prompt to 8 bits", 2047, 2048, "bf16", "bf16", "mx8", 0.0),
+        _norm("norm, prompt, to 8 bits", 2047, 2048, "bf16", "bf16", "mx8", 0.0),
         # a training batch at the 2b sizes: the layer's fp32 output is dropped,
         # added to the bf16 residual stream and normed for the next layer
-        _norm("norm training dropout", 32768, 2304, "f32", "bf16", "bf16", 0.1),
+        _norm("norm, training, dropout", 32768, 2304, "f32", "bf16", "bf16", 0.1),
         # fp32 throughout, odd width
-        _norm("norm odd width f32", 1003, 1001, "f32", "f32", "f32", 0.0),
+        _norm("norm, odd width, f32", 1003, 1001, "f32", "f32", "f32", 0.0),
         # the gradient of the training batch: dy is the layer's fp32 dX
-        _norm_bwd("norm backward training", 32768, 2304, "f32", "bf16", "bf16", 0.1),
+        _norm_bwd("norm backward, training", 32768, 2304, "f32", "bf16", "bf16", 0.1),
         # the gradient of an odd, small fp32 batch
-        _norm_bwd("norm backward odd f32", 777, 1001, "f32", "f32", "f32", 0.25),
+        _norm_bwd("norm backward, odd, f32", 777, 1001, "f32", "f32", "f32", 0.25),
         # the last layer's output added to the residual stream, 1.5b sizes
         _drop("dropout with residual", 16384, 2048, "bf16", "bf16", "bf16", 0.1),
         # the gradient's way through dropout, small and odd
-        _drop("dropout backward odd", 333, 1001, "f32", "none", "f32", 0.25),
+        _drop("dropout backward, odd", 333, 1001, "f32", "none", "f32", 0.25),
         # one token through one projection of the 2b sizes
-        _matvec("4-bit matvec one token", 1, 9216, 2304, "bf16", "f32"),
+        _matvec("4-bit matvec, one token", 1, 9216, 2304, "bf16", "f32"),
         # a batch of tokens into a wide output layer of odd size
-        _matvec("4-bit product 16 tokens wide", 16, 40001, 2048, "mx8", "f32"),
+        _matvec("4-bit product, 16 tokens, wide", 16, 40001, 2048, "mx8", "f32"),
         # one decoded token through the 2b-sized layer
-        _ffn("4-bit layer one token", 1, 2304, 9216, "mx8", "f32", 0.0093),
+        _ffn("4-bit layer, one token", 1, 2304, 9216, "mx8", "f32", 0.0093),
         # a decode batch through the 1.5b-sized layer
-        _ffn("4-bit layer 64 tokens", 64, 2048, 5632, "bf16", "bf16", 0.015),
+        _ffn("4-bit layer, 64 tokens", 64, 2048, 5632, "bf16", "bf16", 0.015),
     ]
 
 
