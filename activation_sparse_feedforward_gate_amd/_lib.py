@@ -542,15 +542,17 @@ def twell_dropout_add(shape: c_twell_norm_shape, x, residual, rng, y, stream=Non
 @dataclass(frozen=True)
 class TwellW4:
     """An MXFP4 weight matrix [N][K] (twell_w4 in include/twell.h): codes
-    [N][K / 2] and scales [N][K / 32], uint8 tensors."""
+    [N][K / 2] and scales [N][K / 32], uint8 tensors (or torch's float4_e2m1fn_x2
+    and float8_e8m0fnu)."""
     codes: object
     scales: object
 
     def __post_init__(self):
+        import torch
         c, s = self.codes, self.scales
-        for t in (c, s):
-            if t.dim() != 2 or t.element_size() != 1 or not t.is_contiguous():
-                raise ValueError(f"TwellW4: expected a contiguous byte matrix, got {tuple(t.shape)} {t.dtype}")
+        for t, own in ((c, torch.float4_e2m1fn_x2), (s, torch.float8_e8m0fnu)):
+            if t.dim() != 2 or t.dtype not in (torch.uint8, own) or not t.is_contiguous():
+                raise ValueError(f"TwellW4: expected a contiguous matrix of uint8 or {own}, got {tuple(t.shape)} {t.dtype}")
         if c.shape[0] != s.shape[0] or c.shape[1] != 16 * s.shape[1]:
             raise ValueError(f"TwellW4: codes {tuple(c.shape)} do not go with scales {tuple(s.shape)}")
 
