@@ -82,9 +82,10 @@ twell_status w4(W4View* v, const twell_w4* W, const char* name) {
   return TWELL_OK;
 }
 
-// Activations of a product with 4-bit weights.
+bool token_dt(int dt) { return dt == TWELL_BF16 || dt == TWELL_MXFP8; }
+
+// Activations of a product with 4-bit weights, of a type that token_dt takes.
 twell_status tokens(W4Args* a, const void* x, int x_dt, const uint8_t* x_scale) {
-  if (x_dt != TWELL_BF16 && x_dt != TWELL_MXFP8) return FAIL(TWELL_EINVAL, "x must be BF16 or MXFP8");
   if ((x_dt == TWELL_MXFP8) != (x_scale != nullptr))
     return FAIL(TWELL_EINVAL, "x_scale goes with an MXFP8 x and with no other");
   if ((uintptr_t)x % dt_size(x_dt)) return FAIL(TWELL_EINVAL, "x is not aligned to its elements");
@@ -173,11 +174,12 @@ twell_status twell_w4_matvec(int32_t T, const void* x, twell_dtype x_dt, int64_t
   W4Args a{};
   if (T < 0) return FAIL(TWELL_EINVAL, "bad T=%d", T);
   CHECK(w4(&a.W, W, "W"));
-  CHECK(tokens(&a, x, x_dt, x_scale));
+  if (!token_dt(x_dt)) return FAIL(TWELL_EINVAL, "x must be BF16 or MXFP8");
   if (!float_dt(y_dt)) return FAIL(TWELL_EINVAL, "y must be F32 or BF16");
+  if (T == 0) return TWELL_OK;
+  CHECK(tokens(&a, x, x_dt, x_scale));
   if ((uintptr_t)y % dt_size(y_dt) || (uintptr_t)bias % 2)
     return FAIL(TWELL_EINVAL, "y or bias is not aligned to its elements");
-  if (T == 0) return TWELL_OK;
   if (!x || !y) return FAIL(TWELL_EINVAL, "NULL tensor argument");
   if (T > 1 && (ldx < W->K || ldy < W->N))
     return FAIL(TWELL_EINVAL, "row stride of x (%lld) or y (%lld) below K=%d or N=%d", (long long)ldx, (long long)ldy,
@@ -196,7 +198,7 @@ twell_status twell_w4_matvec(int32_t T, const void* x, twell_dtype x_dt, int64_t
 static twell_status check_ffn_w4_shape(const twell_ffn_shape* sh) {
   if (!sh) return FAIL(TWELL_EINVAL, "shape is NULL");
   if (sh->T < 0 || sh->d <= 0 || sh->F <= 0) return FAIL(TWELL_EINVAL, "bad shape T=%d d=%d F=%d", sh->T, sh->d, sh->F);
-  if ((sh->in_dt != TWELL_BF16 && sh->in_dt != TWELL_MXFP8) || !float_dt(sh->out_dt))
+  if (!token_dt(sh->in_dt) || !float_dt(sh->out_dt))
     return FAIL(TWELL_EINVAL, "bad dtype (x BF16 or MXFP8, y F32 or BF16)");
   if (sh->d % 64 || sh->F % 64) return FAIL(TWELL_EUNSUPPORTED, "d=%d and F=%d must be multiples of 64", sh->d, sh->F);
   const int64_t lim = (int64_t)1 << 31;

@@ -102,3 +102,10 @@ def test_binding_checks_tensors():
 
 def test_matvec_refuses_rows_past_32_bit_offsets():
     assert _matvec(_w(K=1 << 30), ldx=1 << 30) == tw.TWELL_EUNSUPPORTED
+
+
+def test_no_tokens_is_no_error_in_either_type():
+    """A tensor of no elements has no address; nothing is read or written."""
+    for k in (dict(dt=BF16), dict(dt=MX8), dict(dt=MX8, xs=A)):
+        assert _matvec(_w(), T=0, x=None, y=None, **k) == tw.TWELL_OK, k
+    assert _matvec(_w(), T=0, x=None, y=None, dt=F32) == tw.TWELL_EINVAL     # a type that no product takes
