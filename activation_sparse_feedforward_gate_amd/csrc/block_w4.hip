@@ -20,6 +20,7 @@
 // call: the loops below hold little beside the conversions.
 // 16 tokens, 40001 x 2048 (46 MB): 11.4 us, 4.1 TB/s; 30001 x 4096 (66 MB): 14.5 us,
 // 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.6 us, of which a launch is about four.
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -781,17 +782,34 @@ void with_gemv(const W4Args& a, F f) {
 
 }  // namespace
 
-hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s) {
-  if (use_gemv(a)) {
-    with_gemv(a, [&](auto t, int threads) {
-      w4_gemv_kernel<t.value><<<dim3((a.N + GEMV_ROWS - 1) / GEMV_ROWS), threads, 0, s>>>(a);
-    });
-  } else {
-    with_tile<true>(a, [&](auto c) {
-      using C = decltype(c);
-      w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * tile_waves<C>(a), tile_lds<C>(tile_waves<C>(a)), s>>>(a);
-    });
-  }
+// Rows and tokens of one launch.  A grid holds fewer than 2^32 threads along an axis (32
+// a row at most: 16 rows to eight waves), and the kernels count tokens in 32 bits, with up
+// to TOKEN_GRID tiles added to the last one's.
+constexpr int64_t ROW_RUN = 1 << 26, TOKEN_RUN = 1 << 24;
+
+hipError_t launch_w4_matvec(const W4Args& all, hipStream_t s) {
+  for (int64_t n = 0; n < all.N; n += ROW_RUN)
+    for (int64_t t = 0; t < all.T; t += TOKEN_RUN) {
+      W4Args a = all;
+      a.N = (int)std::min(ROW_RUN, all.N - n);
+      a.T = (int)std::min(TOKEN_RUN, all.T - t);
+      a.x = (const char*)all.x + t * all.ldx * (all.x_scale ? 1 : 2);
+      if (all.x_scale) a.x_scale = all.x_scale + t * (all.K / 32);
+      a.W.code = all.W.code + n * (all.K / 2);
+      a.W.scale = all.W.scale + n * (all.K / 32);
+      if (all.bias) a.bias = all.bias + n;
+      a.y = (char*)all.y + (t * all.ldy + n) * (all.y_bf16 ? 2 : 4);
+      if (use_gemv(a)) {
+        with_gemv(a, [&](auto t, int threads) {
+          w4_gemv_kernel<t.value><<<dim3((a.N + GEMV_ROWS - 1) / GEMV_ROWS), threads, 0, s>>>(a);
+        });
+      } else {
+        with_tile<true>(a, [&](auto c) {
+          using C = decltype(c);
+          w4_matvec_kernel<C><<<tile_grid<C>(a), 64 * tile_waves<C>(a), tile_lds<C>(tile_waves<C>(a)), s>>>(a);
+        });
+      }
+    }
   return hipGetLastError();
 }
 
