@@ -43,6 +43,24 @@ twell_status mat(RowMat* m, const twell_norm_shape* sh, const void* p, int64_t l
   return TWELL_OK;
 }
 
+// Whether a (written) and b share memory.  Exact for one pitch (columns of one wider
+// buffer share none); with two, any common range of addresses counts.
+bool overlap(const RowMat& a, const RowMat& b, int T, int d) {
+  typedef __int128 wide;
+  if (!a.p || !b.p || T <= 0) return false;
+  const wide la = (wide)d * dt_size(a.dt), lb = (wide)d * dt_size(b.dt);           // bytes of a row
+  const wide pa = (wide)a.ld * dt_size(a.dt), pb = (wide)b.ld * dt_size(b.dt);     // and of a row's stride
+  const wide by = (wide)(uintptr_t)b.p - (wide)(uintptr_t)a.p;
+  if (by >= (T - 1) * pa + la || -by >= (T - 1) * pb + lb) return false;
+  if (pa != pb) return true;
+  // row i of a and row j of b share memory where -lb < by + (j - i) pa < la: the least
+  // such j - i, of -T + 1 .. T - 1
+  const wide n = -lb - by, down = n >= 0 ? n / pa : -((-n + pa - 1) / pa);
+  const wide k = down + 1 > 1 - T ? down + 1 : 1 - T;
+  return k < T && by + k * pa < la;
+}
+bool in_place(const RowMat& a, const RowMat& b) { return a.p == b.p && a.ld == b.ld && a.dt == b.dt; }
+
 // The norm's weights; row: a row of type row_dt that stands in where there are none.
 twell_status weights(NormArgs* a, const twell_norm_shape* sh, const void* w, const void* row, int row_dt) {
   a->w = w ? w : row;
@@ -149,6 +167,16 @@ twell_status twell_add_rmsnorm_bwd(const twell_norm_shape* sh, const void* dy, i
     if ((uintptr_t)ws % 16) return FAIL(TWELL_EINVAL, "the workspace must be 16-byte aligned");
   }
   if (sh->T == 0 && !dw) return TWELL_OK;
+  const RowMat in[] = {a.y, a.res, a.sum};
+  for (const RowMat& o : {a.dres, a.x})
+    for (const RowMat& i : in)
+      if (overlap(o, i, sh->T, sh->d) && !in_place(o, i))
+        return FAIL(TWELL_EINVAL, "dres or dx overlaps dy, dsum or sum and is not written in place");
+  if (overlap(a.dres, a.x, sh->T, sh->d)) return FAIL(TWELL_EINVAL, "dres and dx overlap");
+  a.dw_may_reread = true;
+  for (const RowMat& o : {a.dres, a.x})
+    for (const RowMat& i : {a.y, a.sum})
+      if (o.p && o.p == i.p) a.dw_may_reread = false;
   a.rstd_in = rstd;
   a.dw = dw;
   a.part = (float*)ws;

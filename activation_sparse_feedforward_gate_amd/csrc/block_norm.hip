@@ -532,9 +532,10 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
 // Whether dw comes from workgroups of its own: they read dy and sum again, and save the
 // second launch (about 3 us) and the parts.  Rows 1 of 2304: 3.7 us, 7.2 by parts; 500
 // of 4096: 8.7 and 12.4; 777 of 1001 fp32: 8.8 and 10.3; 1024 of 2304: 11.6 and 12.5;
-// 1000 of 8000: 26.6 and 22.4; 2000 of 512: 11.1 and 9.1.
+// 1000 of 8000: 26.6 and 22.4; 2000 of 512: 11.1 and 9.1.  Not where dres or dx is
+// written over dy or sum: other workgroups of the launch would read what is new.
 bool dw_apart(const NormArgs& a) {
-  return a.d >= 8 && a.d <= BWD_MAX_D && a.T <= 1024 && (int64_t)a.T * a.d <= 4 << 20;
+  return a.dw_may_reread && a.d >= 8 && a.d <= BWD_MAX_D && a.T <= 1024 && (int64_t)a.T * a.d <= 4 << 20;
 }
 
 int norm_bwd_parts(int T, int d) {

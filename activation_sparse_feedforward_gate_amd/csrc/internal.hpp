@@ -264,6 +264,7 @@ struct NormArgs {
   float* dw;
   float* part;               // [norm_bwd_parts(T, d)][d] row sums of dw, or null
   int dw_blocks;             // workgroups that compute dw without them
+  bool dw_may_reread;        // dy and sum stay as they are while the rows are written
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 int norm_bwd_parts(int T, int d);

@@ -569,8 +569,11 @@ size_t twell_add_rmsnorm_bwd_workspace(const twell_norm_shape *sh);
  *     dx   = dropout(dres), the forward's mask  (gradient of x)
  *     dw   = sum over the rows of dy * xh       (fp32, a fixed order)
  *   dsum  [T][d] or NULL (zeros);  w, rng as in the forward
- *   dres  [T][d] in res_dt, may be dsum itself; may be NULL when dx is given
+ *   dres  [T][d] in res_dt; may be NULL when dx is given
  *   dx    [T][d] in x_dt; may be NULL when dres is given
+ *         Each may be dsum, sum or dy itself where dtype and stride agree (over
+ *         dy or sum, up to 1024 rows take the two launches of more rows for dw).
+ *         Another overlap with those, or of dres with dx, is refused
  *   dw    [d] fp32 or NULL; zeros when T == 0
  *   ws    twell_add_rmsnorm_bwd_workspace(sh) bytes, 16-byte aligned (used for
  *         dw only)
