@@ -1,7 +1,8 @@
 """Build libtwell.so in-tree: every HIP/C++ source under csrc/ is compiled for
 gfx950 with hipcc and linked into activation_sparse_feedforward_gate_amd/lib/;
-and beside it _twell_bind, the Python module that marshals tensors for some of
-its calls (csrc/bind.cpp, host code).
+and after it _twell_bind, the Python module that marshals tensors for some of
+its calls (csrc/bind.cpp, host code), where torch and its headers are there: the
+library itself and its C ABI need hipcc alone.
 
     python -m activation_sparse_feedforward_gate_amd.build [--jobs N]
 """
@@ -43,30 +44,23 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_bind() -> str:
+def _build_bind() -> None:
     import torch
     from torch.utils.cpp_extension import include_paths
-    obj = os.path.join(BUILD, "bind.o")
+    obj, tmp = os.path.join(BUILD, "bind.o"), BIND + ".tmp"
     inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
            os.path.join(ROOT, "include")]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *[f for i in inc for f in ("-isystem", i)], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stderr}")
-    return obj
-
-
-def _link_bind(obj: str) -> None:
-    import torch
     tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BIND + ".tmp"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + LIBDIR, "-ltwell", "-L" + tlib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
+    for what, cmd in (
+            ("compile", [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+                         "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                         *[f for i in inc for f in ("-isystem", i)], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]),
+            ("link", [HIPCC, "-shared", "-no-hip-rt", "-o", tmp, obj, "-L" + LIBDIR, "-ltwell", "-L" + tlib, "-ltorch_python", "-ltorch",
+                      "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} of bind.cpp failed:\n{r.stderr}")
     os.replace(tmp, BIND)
 
 
@@ -74,18 +68,23 @@ def build(jobs: int = 8, verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
-        bind = bind.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_bind(bind)
     if verbose:
         print(f"built {LIB}")
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("torch is not importable: the Python module that marshals its tensors is not built")
+        return LIB
+    _build_bind()
+    if verbose:
+        print(f"built {BIND}")
     return LIB
 
 
