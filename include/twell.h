@@ -602,6 +602,9 @@ twell_status twell_dropout_add(const twell_norm_shape *sh, const void *x, int64_
  *   codes   uint8 [N][K / 2]   two values a byte, the even column in the low
  *                              four bits; 16-byte aligned
  *   scales  uint8 [N][K / 32]  byte b stands for 2^(b - 127), 255 for NaN
+ * A weight, or an MXFP8 token's value, (its code times its scale) of magnitude
+ * below 2^-126 may be taken as 0 or lose its last bits; one of 2^128 or more is
+ * an infinity.  All others are exact.
  */
 typedef struct {
   int32_t N, K;
