@@ -4,9 +4,17 @@
 // operations a value beside the random numbers.
 //
 // Rows are held in registers between the row's sum and its use, so every byte
-// is read and written once.  LPR lanes take a row, CH chunks of eight columns
-// each; LPR <= 64 needs no barrier, and 256 / LPR rows share a workgroup where
-// LPR < 256.
+// is read and written once: in the forward up to 16384 columns, in the backward
+// up to 8192 (and once more for dw up to 1024 rows).  LPR lanes take a row, CH
+// chunks of eight columns each; LPR <= 64 needs no barrier, and 256 / LPR rows
+// share a workgroup where LPR < 256.
+// Wider rows do not fit the 128 registers a lane of 1024 threads, and part of
+// them goes through scratch memory (forward to 32768 columns 9 to 51 registers a
+// lane, beyond 174 to 252; backward to 16384 16 to 35); beyond 16384 columns the
+// backward reads its rows twice instead.  75 million values, fp32 x or dy, bf16
+// rest, dropout: forward 129 us at 2304 columns, 153 at 12288, 145 at 16384, 188
+// at 32768, 454 at 65536; backward 180 at 2304, 171 at 8192, 181 at 12288, 179 at
+// 16384, 369 at 16392, 350 at 32768, 392 at 65536.
 #include "internal.hpp"
 #include "row_ops.hpp"
 
@@ -471,10 +479,11 @@ struct Cfg {
 // Few chunks per lane and few idle lanes: two or three chunks in flight per lane
 // fill the memory pipe, more cost registers and so waves.  32768 rows of 2304
 // (fp32 x, bf16 rest, dropout): <128, 3> 129 us (5.8 TB/s), <256, 2> 144, <64, 5>
-// 166, <64, 8> 273.  Up to 1024 rows the time is one row's latency and one chunk a
-// lane is fastest: 1 row of 2304 to MXFP8, <512, 1> 3.3 us, <256, 2> 4.2, <128, 3> 5.2;
-// 700 rows of 2048, <256, 1> 4.7, <128, 2> 5.5; 1024 of 2304, 8.0 and 8.0; 1500 of
-// 4096, 12.5 and 12.3.
+// 166, <64, 8> 273; 26810 rows of 2816, <128, 3> 130 and <256, 2> 127 (bf16 x, no
+// dropout: 104 and 105).  Up to 1024 rows the time is one row's latency and one chunk
+// a lane is fastest: 1 row of 2304 to MXFP8 in a graph, <512, 1> 3.3 us, <128, 3> 4.6;
+// fp32 x with dropout, 700 rows of 2048, <256, 1> 5.3, <128, 2> 5.8; 1024 of 2304, 7.6
+// and 8.0; 1500 of 4096, 12.4 and 11.9.
 template <class F>
 void with_fwd_cfg(int T, int d, F f) {
   if (d < 8) return f(Cfg<16, 1, true>{});
@@ -530,10 +539,11 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
 }
 
 // Whether dw comes from workgroups of its own: they read dy and sum again, and save the
-// second launch (about 3 us) and the parts.  Rows 1 of 2304: 3.7 us, 7.2 by parts; 500
-// of 4096: 8.7 and 12.4; 777 of 1001 fp32: 8.8 and 10.3; 1024 of 2304: 11.6 and 12.5;
-// 1000 of 8000: 26.6 and 22.4; 2000 of 512: 11.1 and 9.1.  Not where dres or dx is
-// written over dy or sum: other workgroups of the launch would read what is new.
+// second launch and the parts.  fp32 dy, bf16 rest, dropout, 1 row of 2304: 4.0 us, 7.0
+// by parts; 500 of 4096: 9.8 and 12.9; 1024 of 2304: 11.7 and 12.7; 777 of 1001, all
+// fp32: 8.8 and 10.0; 1000 of 8000: 31.2 and 27.2; 2000 of 512: 11.2 and 9.3.  Not where
+// dres or dx is written over dy or sum: other workgroups of the launch would read what
+// is new.
 bool dw_apart(const NormArgs& a) {
   return a.dw_may_reread && a.d >= 8 && a.d <= BWD_MAX_D && a.T <= 1024 && (int64_t)a.T * a.d <= 4 << 20;
 }

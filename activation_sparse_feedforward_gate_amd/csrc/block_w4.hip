@@ -19,7 +19,8 @@
 // than others), so a few hundred of them are as long as the memory's part of a small
 // call: the loops below hold little beside the conversions.
 // 16 tokens, 40001 x 2048 (46 MB): 11.4 us, 4.1 TB/s; 30001 x 4096 (66 MB): 14.5 us,
-// 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.6 us, of which a launch is about four.
+// 4.5 TB/s; one token, 9216 x 2304 (11 MB): 4.6 us, one round of loads and the sums over
+// the waves (in a graph the shortest kernel takes 1.6 us a launch).
 #include <algorithm>
 #include <type_traits>
 
@@ -698,7 +699,8 @@ namespace {
 
 // Calls f with the tile for the tokens and rows.  32 rows x 16 tokens, unless there is
 // no more than one workgroup of 16 x 16 for each CU, or more than 16 tokens go with
-// enough rows of a product for tiles that read them half as often (the layer's list of
+// enough rows of a product for tiles that read them half as often and still are many (the
+// borders in rows were measured with 20 to 64 tokens; the layer's list of
 // rows that fire grows with its tile).  With the tile of the neighbouring range: 30
 // tokens, 700 x 8192, 6.2 us and 9.1 (small); 64 tokens, 2048 x 2048, 4.3 and 5.0
 // (narrow); 9216 x 2304, 11.4 and 11.8 (middle); 12000 x 2048, 11.9 and 14.3 (small);

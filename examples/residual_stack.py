@@ -30,7 +30,6 @@ import activation_sparse_feedforward_gate_amd as tw  # noqa: E402
 
 BF16, F32, MX8 = tw.TWELL_BF16, tw.TWELL_F32, tw.TWELL_MXFP8
 EPS = 1e-5
-FP4 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 
 def empty(*size, dt=torch.bfloat16):

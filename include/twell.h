@@ -521,7 +521,8 @@ twell_status twell_ffn_fwd_noalloc(const twell_ffn_shape *sh, const void *x, con
  *   p       probability of a value being dropped, 0 <= p <= 1, taken to the
  *           nearest multiple of 2^-16; 0 switches dropout off
  * Each matrix argument is followed by its row stride in elements (>= d; ignored
- * for T <= 1).  Pointers need the alignment of their elements only.
+ * for T <= 1).  Pointers need the alignment of their elements only.  An output
+ * shares memory with no other argument but where its call names it.
  *
  * Dropout takes its random numbers from a counter-based generator, so no mask
  * is stored: Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw,
@@ -633,8 +634,11 @@ size_t twell_ffn_fwd_w4_workspace(const twell_ffn_shape *sh);
 /*
  * twell_ffn_fwd_w4: the layer of twell_ffn_fwd on MXFP4 weights Wg, Wu and Wd
  * (each N = F, K = d), for the few tokens of a serving step: of Wu and Wd only
- * the rows of neurons that fire (g > 0 in fp32) are read.  in_dt BF16 or MXFP8 (of x), out_dt F32 or BF16;
- * products and h, u, a are accumulated and kept in fp32.
+ * the rows of neurons that fire (g > 0 in fp32) are read.  in_dt BF16 or MXFP8
+ * (of x), out_dt F32 or BF16; products and h, u, a are accumulated and kept in
+ * fp32.  All three matrices have their scales along d: for Wg and Wu that is what
+ * their products sum over, for Wd the columns of y, so that a row is read whole
+ * where its neuron fires.  A Wd with scales along F has to be quantised again.
  *   x        [T][d]; x_scale [T][d / 32] for MXFP8, NULL for BF16
  *   bg       [F] BF16 or NULL
  *   y        [T][d]
